@@ -29,7 +29,9 @@ EXPORTS = ("hils_status_string", "hils_version", "hils_validate", "hils_describe
            "hils_chunk_attend_fuse", "hils_forward", "hils_forward_host_workspace_size", "hils_forward_host", "hils_sync_status", "hils_set_wait_limit",
            "hils_decode_score_select_noalloc", "hils_debug_inject_stall", "hils_landmarks",
            "hils_score_select_window", "hils_forward_window_workspace_size", "hils_forward_window",
-           "hils_backward")
+           "hils_backward", "hils_cache_append_q8", "hils_cache_read_q8", "hils_landmarks_q8",
+           "hils_chunk_attend_fuse_q8_workspace_size", "hils_chunk_attend_fuse_q8", "hils_forward_q8_workspace_size",
+           "hils_forward_q8")
 HILS_NOALLOC_SCRATCH_BYTES = 1 << 20
 
 
@@ -79,6 +81,13 @@ def _load():
     lib.hils_forward_window_workspace_size.argtypes = [P, ci, ctypes.POINTER(sz)]
     lib.hils_forward_window.argtypes = [P, ci, vp, vp, vp, vp, vp, vp, vp, sz, vp]
     lib.hils_backward.argtypes = [P, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp]
+    lib.hils_cache_append_q8.argtypes = [P, vp, vp, vp, vp, vp, vp, ci, ci, vp]
+    lib.hils_cache_read_q8.argtypes = [P, vp, vp, vp, vp, vp, vp, ci, ci, vp]
+    lib.hils_landmarks_q8.argtypes = [P, vp, vp, vp, vp, vp, ci, ci, ci, vp]
+    lib.hils_chunk_attend_fuse_q8_workspace_size.argtypes = [P, ctypes.POINTER(sz)]
+    lib.hils_chunk_attend_fuse_q8.argtypes = [P, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
+    lib.hils_forward_q8_workspace_size.argtypes = [P, ctypes.POINTER(sz)]
+    lib.hils_forward_q8.argtypes = [P, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
     for n in EXPORTS[2:]:
         if n not in ("hils_status_string", "hils_version"):
             getattr(lib, n).restype = ctypes.c_int
@@ -253,6 +262,53 @@ def hils_backward(p, Q, K, V, L, sel_idx, dO, dQ, dK, dV, dL, stream=None):
     """Gradients dQ, dK, dV, dL (float32 tensors, written) of sum(O * dO) through the selection sel_idx."""
     _check(_lib.hils_backward(ctypes.byref(p), _ptr(Q), _ptr(K), _ptr(V), _ptr(L), _ptr(sel_idx), _ptr(dO), _ptr(dQ),
                               _ptr(dK), _ptr(dV), _ptr(dL), _stream(stream)), "hils_backward")
+
+
+def hils_cache_append_q8(p, K, V, K8, V8, k_scale, v_scale, t_begin, t_end, stream=None):
+    """Write tokens [t_begin, t_end), K and V [B,Hkv,t_end-t_begin,d], into the 8-bit cache: e4m3 bytes K8, V8 [B,Hkv,T,d]
+    (any one-byte dtype) with a float32 scale per chunk, k_scale and v_scale [B,Hkv,nL]; see include/hils.h."""
+    _check(_lib.hils_cache_append_q8(ctypes.byref(p), _ptr(K), _ptr(V), _ptr(K8), _ptr(V8), _ptr(k_scale), _ptr(v_scale),
+                                     int(t_begin), int(t_end), _stream(stream)), "hils_cache_append_q8")
+
+
+def hils_cache_read_q8(p, K8, V8, k_scale, v_scale, K, V, t_begin, t_end, stream=None):
+    """Read tokens [t_begin, t_end) of the 8-bit cache into K and V [B,Hkv,t_end-t_begin,d] (in_dtype)."""
+    _check(_lib.hils_cache_read_q8(ctypes.byref(p), _ptr(K8), _ptr(V8), _ptr(k_scale), _ptr(v_scale), _ptr(K), _ptr(V),
+                                   int(t_begin), int(t_end), _stream(stream)), "hils_cache_read_q8")
+
+
+def hils_landmarks_q8(p, K8, k_scale, U, L, beta=None, c_begin=0, c_end=None, t_end=None, stream=None):
+    """hils_landmarks from the keys of the 8-bit cache, which holds t_end tokens (default T); c_end defaults to the
+    number of chunks they touch."""
+    if t_end is None:
+        t_end = p.T
+    if c_end is None:
+        c_end = (t_end + p.C - 1) // p.C
+    _check(_lib.hils_landmarks_q8(ctypes.byref(p), _ptr(K8), _ptr(k_scale), _ptr(U), _ptr(L), _ptr(beta), int(c_begin),
+                                  int(c_end), int(t_end), _stream(stream)), "hils_landmarks_q8")
+
+
+def hils_chunk_attend_fuse_q8_workspace_size(p):
+    return _size(_lib.hils_chunk_attend_fuse_q8_workspace_size, p)
+
+
+def hils_chunk_attend_fuse_q8(p, Q, K8, V8, k_scale, v_scale, sel_idx, sel_score, O, workspace=None, stream=None):
+    """hils_chunk_attend_fuse over the 8-bit cache."""
+    wp, wn = _ws(workspace)
+    _check(_lib.hils_chunk_attend_fuse_q8(ctypes.byref(p), _ptr(Q), _ptr(K8), _ptr(V8), _ptr(k_scale), _ptr(v_scale),
+                                          _ptr(sel_idx), _ptr(sel_score), _ptr(O), wp, wn, _stream(stream)),
+           "hils_chunk_attend_fuse_q8")
+
+
+def hils_forward_q8_workspace_size(p):
+    return _size(_lib.hils_forward_q8_workspace_size, p)
+
+
+def hils_forward_q8(p, Q, K8, V8, k_scale, v_scale, L, O, workspace=None, stream=None):
+    """hils_forward over the 8-bit cache (landmarks L in in_dtype)."""
+    wp, wn = _ws(workspace)
+    _check(_lib.hils_forward_q8(ctypes.byref(p), _ptr(Q), _ptr(K8), _ptr(V8), _ptr(k_scale), _ptr(v_scale), _ptr(L),
+                                _ptr(O), wp, wn, _stream(stream)), "hils_forward_q8")
 
 
 def problem(B, H, Hkv, N, T, d, C, k, q_offset=0, in_dtype=HILS_BF16, out_dtype=None, scale=0.0):

@@ -5,6 +5,7 @@
 #include <string.h>
 #include <mutex>
 
+#include "cache8.h"
 #include "internal.h"
 #include "next_rows.h"
 
@@ -665,6 +666,157 @@ hils_status hils_backward(const hils_problem *p, const void *Q, const void *K, c
     if ((long long)d.B * d.Hkv * d.N > 0x7FFFFFFFll) return HILS_ERR_UNSUPPORTED;
     return from_cuda(launch_backward(d, p->in_dtype, Q, K, V, L, sel_idx, dO, dQ, dK, dV, dL,
                                      static_cast<cudaStream_t>(stream)));
+}
+
+// ---- the 8-bit cache ---------------------------------------------------------------------------------------
+
+// What the cache's own calls check of a problem: B, Hkv, T, d, C and in_dtype; the other fields are ignored.
+static hils_status resolve_cache8(const hils_problem *p, Cache8 *c)
+{
+    if (!p) return HILS_ERR_INVALID_ARG;
+    if (p->B < 1 || p->Hkv < 1 || p->T < 1 || p->C < 1 || p->d < 1) return HILS_ERR_INVALID_ARG;
+    if (p->in_dtype != HILS_F32 && p->in_dtype != HILS_BF16) return HILS_ERR_INVALID_ARG;
+    if (p->d != 64 && p->d != 128) return HILS_ERR_UNSUPPORTED;
+    if (p->C != 32 && p->C != 64 && p->C != 128) return HILS_ERR_UNSUPPORTED;
+    if ((long long)p->B * p->Hkv > 65535) return HILS_ERR_UNSUPPORTED;
+    c->B = p->B; c->Hkv = p->Hkv; c->T = p->T; c->d = p->d; c->C = p->C;
+    c->nL = (int)(((long long)p->T + p->C - 1) / p->C);
+    return HILS_OK;
+}
+
+// A range of tokens and the pointers of both sides.
+static hils_status check_cache8(const Cache8 &c, const void *K, const void *V, const void *K8, const void *V8,
+                                const float *ks, const float *vs, int t_begin, int t_end)
+{
+    if (t_begin < 0 || t_end < t_begin || t_end > c.T) return HILS_ERR_INVALID_ARG;
+    if (!K || !V || !K8 || !V8 || !ks || !vs) return HILS_ERR_INVALID_ARG;
+    if (!aligned16(K) || !aligned16(V) || !aligned16(K8) || !aligned16(V8) || !aligned4(ks) || !aligned4(vs))
+        return HILS_ERR_INVALID_ARG;
+    if (2ll * c.B * c.Hkv * c.nL > 0x7FFFFFFFll) return HILS_ERR_UNSUPPORTED;
+    return HILS_OK;
+}
+
+hils_status hils_cache_append_q8(const hils_problem *p, const void *K, const void *V, void *K8, void *V8, float *k_scale,
+                                 float *v_scale, int t_begin, int t_end, void *stream)
+{
+    Cache8 c;
+    hils_status st = resolve_cache8(p, &c);
+    if (st == HILS_OK) st = check_cache8(c, K, V, K8, V8, k_scale, v_scale, t_begin, t_end);
+    if (st != HILS_OK || t_begin == t_end) return st;
+    return from_cuda(launch_cache_append(c, p->in_dtype, K, V, static_cast<uint8_t *>(K8), static_cast<uint8_t *>(V8),
+                                         k_scale, v_scale, t_begin, t_end, static_cast<cudaStream_t>(stream)));
+}
+
+hils_status hils_cache_read_q8(const hils_problem *p, const void *K8, const void *V8, const float *k_scale,
+                               const float *v_scale, void *K, void *V, int t_begin, int t_end, void *stream)
+{
+    Cache8 c;
+    hils_status st = resolve_cache8(p, &c);
+    if (st == HILS_OK) st = check_cache8(c, K, V, K8, V8, k_scale, v_scale, t_begin, t_end);
+    if (st != HILS_OK || t_begin == t_end) return st;
+    return from_cuda(launch_cache_read(c, p->in_dtype, static_cast<const uint8_t *>(K8), static_cast<const uint8_t *>(V8),
+                                       k_scale, v_scale, K, V, t_begin, t_end, static_cast<cudaStream_t>(stream)));
+}
+
+hils_status hils_landmarks_q8(const hils_problem *p, const void *K8, const float *k_scale, const void *U, void *L,
+                              float *beta, int c_begin, int c_end, int t_end, void *stream)
+{
+    Cache8 c;
+    const hils_status st = resolve_cache8(p, &c);
+    if (st != HILS_OK) return st;
+    if (!(p->scale >= 0.f) || isinf(p->scale)) return HILS_ERR_INVALID_ARG;
+    if (t_end < 1 || t_end > c.T) return HILS_ERR_INVALID_ARG;
+    if (c_begin < 0 || c_end < c_begin || c_end > ((long long)t_end + c.C - 1) / c.C) return HILS_ERR_INVALID_ARG;
+    if (!K8 || !k_scale || !U || !L) return HILS_ERR_INVALID_ARG;
+    if (!aligned16(K8) || !aligned4(k_scale) || !aligned16(U) || !aligned16(L) || !aligned4(beta))
+        return HILS_ERR_INVALID_ARG;
+    if ((long long)c.B * c.Hkv * c.nL > 0x7FFFFFFFll) return HILS_ERR_UNSUPPORTED;
+    if (c_begin == c_end) return HILS_OK;
+    const float scale = p->scale > 0.f ? p->scale : 1.0f / sqrtf((float)p->d);
+    return from_cuda(launch_landmarks8(c, p->in_dtype, scale, static_cast<const uint8_t *>(K8), k_scale, U, L, beta, c_begin,
+                                       c_end, t_end, static_cast<cudaStream_t>(stream)));
+}
+
+static bool aligned_cache8(const void *K8, const void *V8, const float *ks, const float *vs)
+{
+    return aligned16(K8) && aligned16(V8) && aligned4(ks) && aligned4(vs);
+}
+
+hils_status hils_chunk_attend_fuse_q8_workspace_size(const hils_problem *p, size_t *bytes)
+{
+    Dims d;
+    if (!bytes) return HILS_ERR_INVALID_ARG;
+    const hils_status st = resolve(p, &d);
+    if (st != HILS_OK) return st;
+    *bytes = attend8_ws_bytes(d, p->in_dtype, p->out_dtype);
+    return HILS_OK;
+}
+
+hils_status hils_chunk_attend_fuse_q8(const hils_problem *p, const void *Q, const void *K8, const void *V8,
+                                      const float *k_scale, const float *v_scale, const int32_t *sel_idx,
+                                      const float *sel_score, void *O, void *workspace, size_t workspace_bytes,
+                                      void *stream)
+{
+    Dims d;
+    hils_status st = resolve(p, &d);
+    if (st != HILS_OK) return st;
+    if (!Q || !K8 || !V8 || !k_scale || !v_scale || !sel_score || !O || (d.k > 0 && !sel_idx)) return HILS_ERR_INVALID_ARG;
+    if (!aligned16(Q) || !aligned_cache8(K8, V8, k_scale, v_scale) || !aligned16(O) || !aligned16(sel_score) ||
+        (sel_idx && !aligned16(sel_idx)))
+        return HILS_ERR_INVALID_ARG;
+    st = check_ws(workspace, workspace_bytes, attend8_ws_bytes(d, p->in_dtype, p->out_dtype));
+    if (st != HILS_OK) return st;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (check_caller_selection()) {
+        st = check_selection(d, sel_idx, s);
+        if (st != HILS_OK) return st;
+    }
+    DeviceCtl ctl;
+    st = device_ctl(&ctl);
+    if (st != HILS_OK) return st;
+    return from_cuda(launch_attend8(d, p->in_dtype, p->out_dtype, Q, static_cast<const uint8_t *>(K8),
+                                    static_cast<const uint8_t *>(V8), k_scale, v_scale, sel_idx, sel_score, O, workspace,
+                                    ctl, s));
+}
+
+hils_status hils_forward_q8_workspace_size(const hils_problem *p, size_t *bytes)
+{
+    Dims d;
+    if (!bytes) return HILS_ERR_INVALID_ARG;
+    const hils_status st = resolve(p, &d);
+    if (st != HILS_OK) return st;
+    const size_t sel = select_ws(d), att = attend8_ws_bytes(d, p->in_dtype, p->out_dtype);
+    *bytes = sel_idx_bytes(d) + sel_score_bytes(d) + (sel > att ? sel : att);
+    return HILS_OK;
+}
+
+hils_status hils_forward_q8(const hils_problem *p, const void *Q, const void *K8, const void *V8, const float *k_scale,
+                            const float *v_scale, const void *L, void *O, void *workspace, size_t workspace_bytes,
+                            void *stream)
+{
+    Dims d;
+    hils_status st = resolve(p, &d);
+    if (st != HILS_OK) return st;
+    if (!Q || !K8 || !V8 || !k_scale || !v_scale || !L || !O) return HILS_ERR_INVALID_ARG;
+    if (!aligned16(Q) || !aligned_cache8(K8, V8, k_scale, v_scale) || !aligned16(L) || !aligned16(O))
+        return HILS_ERR_INVALID_ARG;
+    size_t need = 0;
+    hils_forward_q8_workspace_size(p, &need);
+    st = check_ws(workspace, workspace_bytes, need);
+    if (st != HILS_OK) return st;
+    char *ws = static_cast<char *>(workspace);
+    int32_t *sel_idx = reinterpret_cast<int32_t *>(ws);
+    float *sel_score = reinterpret_cast<float *>(ws + sel_idx_bytes(d));
+    void *scratch = ws + sel_idx_bytes(d) + sel_score_bytes(d);
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    st = do_select(d, p->in_dtype, Q, L, sel_idx, sel_score, scratch, s);
+    if (st != HILS_OK) return st;
+    DeviceCtl ctl;
+    st = device_ctl(&ctl);
+    if (st != HILS_OK) return st;
+    return from_cuda(launch_attend8(d, p->in_dtype, p->out_dtype, Q, static_cast<const uint8_t *>(K8),
+                                    static_cast<const uint8_t *>(V8), k_scale, v_scale, sel_idx, sel_score, O, scratch, ctl,
+                                    s));
 }
 
 hils_status hils_sync_status(void *stream)

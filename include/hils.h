@@ -282,6 +282,88 @@ HILS_API hils_status hils_backward(const hils_problem *p, const void *Q, const v
                                    float *dK, float *dV, float *dL, void *stream);
 
 /*
+ * ---- The 8-bit cache -------------------------------------------------------
+ * Keys and values as e4m3 bytes with one float scale for each chunk of each
+ * (b, kv-head), on each side: half the bytes of a bf16 cache, and of the
+ * chunks that decode gathers.  The method's steps are the same, on keys
+ * k_scale[c] * K8[t] and values v_scale[c] * V8[t], c = t / C.  Landmarks and
+ * selection stay in in_dtype.
+ *   K8, V8            [B][Hkv][T][d]  e4m3: sign, 4 exponent bits (bias 7),
+ *                                     3 fraction bits, 0x7F / 0xFF NaN
+ *   k_scale, v_scale  [B][Hkv][nL]    float
+ * all in device memory, owned by the caller, K8 and V8 16-byte aligned, the
+ * scales 4-byte aligned.  T is the cache's capacity: a sequence fills it from
+ * token 0, and what stands behind its last token (bytes, and the scales of
+ * chunks without a token) is never read as data and may be anything.
+ * d is 64 or 128 and C 32, 64 or 128 (else HILS_ERR_UNSUPPORTED).
+ */
+
+/*
+ * Write tokens [t_begin, t_end) into the cache.  K, V [B][Hkv][t_end - t_begin][d]
+ * in in_dtype.  Per side, (b, kv-head) and chunk the range touches:
+ *   m = the largest magnitude of the chunk's new rows (infinities and NaN left out)
+ *   e = the smallest integer in -100 .. 119 with m <= 448 * 2^e
+ *   s = 2^e, or max(2^e, the chunk's scale) when the chunk holds rows before t_begin
+ * New rows become e4m3(x / s), to nearest even; infinities and what lies beyond
+ * 448 s become +-448, NaN stays NaN.  Where s is above the chunk's scale, its
+ * rows before t_begin become e4m3(code * scale / s): exact, the scales being
+ * powers of two, but for values that become subnormal.  So token by token and
+ * all at once give the same bytes but for such values.  A chunk that the range
+ * starts (t_begin <= c * C) takes nothing from its old bytes and scale; rows
+ * behind t_end keep their bytes.  Uses B, Hkv, T, d, C and in_dtype of p;
+ * 0 <= t_begin <= t_end <= T (else HILS_ERR_INVALID_ARG; an empty range
+ * launches nothing).  Calls that write the same chunk must not overlap.
+ * Asynchronous on `stream`; no workspace.
+ */
+HILS_API hils_status hils_cache_append_q8(const hils_problem *p, const void *K, const void *V, void *K8, void *V8,
+                                          float *k_scale, float *v_scale, int t_begin, int t_end, void *stream);
+
+/*
+ * Read tokens [t_begin, t_end) back: K, V [B][Hkv][t_end - t_begin][d] in
+ * in_dtype, scale * value rounded once (exact for scales that an append wrote,
+ * as long as it stays in in_dtype's range).  The tokens must have been written.
+ * Arguments as for hils_cache_append_q8; K and V must not overlap K8 and V8.
+ */
+HILS_API hils_status hils_cache_read_q8(const hils_problem *p, const void *K8, const void *V8, const float *k_scale,
+                                        const float *v_scale, void *K, void *V, int t_begin, int t_end, void *stream);
+
+/*
+ * hils_landmarks from the 8-bit keys: L and beta of chunks [c_begin, c_end) from
+ * the chunk's rows below t_end, the number of tokens in the cache (1 <= t_end
+ * <= T, c_end <= ceil(t_end / C), so that every chunk asked for holds a row).
+ * U [B][Hkv][nL][d] and L [B][Hkv][nL][d] in in_dtype, beta float or NULL.
+ * A decode step that completes chunk c calls it with c, c + 1, (c + 1) * C.
+ */
+HILS_API hils_status hils_landmarks_q8(const hils_problem *p, const void *K8, const float *k_scale, const void *U,
+                                       void *L, float *beta, int c_begin, int c_end, int t_end, void *stream);
+
+/*
+ * hils_chunk_attend_fuse over the 8-bit cache, with the same selection
+ * arguments (also those of hils_score_select_window, on its k'), ownership and
+ * errors.  A slot with sel_idx -1 is empty whatever its score, and a slot with
+ * score -INFINITY has no weight; a row without any weight is zero.  The scales
+ * may be any finite floats.  The result is defined when the bytes the call's
+ * queries may see (t < q_offset + N, in selected chunks) hold no NaN and the
+ * products stay in float range; bytes behind them may be anything.
+ * Precision: products accumulate in float32.
+ */
+HILS_API hils_status hils_chunk_attend_fuse_q8_workspace_size(const hils_problem *p, size_t *bytes);
+HILS_API hils_status hils_chunk_attend_fuse_q8(const hils_problem *p, const void *Q, const void *K8, const void *V8,
+                                               const float *k_scale, const float *v_scale, const int32_t *sel_idx,
+                                               const float *sel_score, void *O, void *workspace, size_t workspace_bytes,
+                                               void *stream);
+
+/*
+ * The forward pass over the 8-bit cache: hils_score_select, then
+ * hils_chunk_attend_fuse_q8, the selection kept in the workspace.  N = 1 is
+ * single-token decode.
+ */
+HILS_API hils_status hils_forward_q8_workspace_size(const hils_problem *p, size_t *bytes);
+HILS_API hils_status hils_forward_q8(const hils_problem *p, const void *Q, const void *K8, const void *V8,
+                                     const float *k_scale, const float *v_scale, const void *L, void *O,
+                                     void *workspace, size_t workspace_bytes, void *stream);
+
+/*
  * Synchronise `stream` and report device-side status since the last call:
  * HILS_ERR_TIMEOUT if a bounded wait inside a kernel gave up (the kernel then
  * skipped its remaining work and released its resources), HILS_ERR_CUDA if
