@@ -1,93 +1,432 @@
-// attend8.cu -- chunk attention and fusion over the 8-bit cache (CUDA cores, every shape).
+// attend8.cu -- chunk attention and fusion over the 8-bit cache, a row of work per query group: single-token decode,
+// few queries, and every shape and type.
 //
 // "Hierarchical Sparse Attention Done Right" (arXiv 2607.02980v1), Abstract and Sec. 3 "Hierarchical softmax", with
-// keys ks_c e and values vs_c e' (e4m3 rows e, e', one scale per chunk and side): the chunk's logits carry
-// scale * ks_c, its output carries the fusion weight times vs_c.
+// keys ks_c e and values vs_c e' (e4m3 rows e, e', one scale per chunk and side):
+//   x_j = (scale ks_c) <q, e_j>,  p = softmax_j(x) over the keys seen,  o = sum_c (w_c vs_c) sum_j p_j e'_j.
+// Every selected chunk is 2 C d bytes that one query group uses once, so the kernel's job is to keep loads in
+// flight; the products run on mma.sync tiles (4 heads x 64 keys x 128 columns is far below a tcgen05 tile).
 //
-// One block per query group (b, g, i), one warp per head; a chunk's visible rows are widened to float32 in shared
-// memory once for the group's heads.
+// One warp takes a whole chunk at a time, straight from global memory into registers: no shared-memory tiles,
+// because e4m3 bytes have to pass through registers anyway to become f16 (exact), and because the index orders of an
+// mma product are free: the d index of Q K^T and the d rows of V^T P are permuted so that what a lane's 16-byte loads
+// bring is what its fragments hold.
+//   S^T = K Q^T     A = 16 keys x 16 of d, B = 8 heads: lane (r, t) = (lane / 4, lane % 4) loads 16 bytes of keys r
+//                   and r + 8 at d = 64 s + 16 t, whose words are its A fragments of four k-steps
+//   O^T = V^T P^T   A = 16 of d x 16 keys: the lane loads 16 bytes at d = 16 r of keys 2t, 2t+1, 2t+8, 2t+9; byte
+//                   permutes pair the keys; P^T comes from S^T's accumulators by movmatrix
+// The eight columns are heads: a group of more than eight is two rows of work.  While a chunk's probabilities are
+// made the next chunk's keys are on their way, and its values during the next chunk's scores, so a warp
+// keeps 8 to 16 KB in flight.
+//
+// Numbers.  A query row is scaled by a power of two to just below 2^15 and taken in f16: bf16 queries keep their 8 bits down
+// to 2^-29 of the row's largest, and below that an error of 2^-39 of it; float32 queries are two f16 pieces (22 bits).
+// P carries w_c vs_c / max_c'(w vs) and a factor 2^14 into f16 (2^-12 of the value down to 2^-28 of the row's
+// largest weight); for float32 results it is two f16 pieces.  All sums are float32.
+//
+// A row's slots are split over the warps of one block or of a cluster of blocks, and the partial rows meet in shared
+// memory (distributed shared memory for a cluster): no workspace, no atomics, a fixed order.
 #include "attend_simt.cuh"
 #include "cache8.h"
 #include "e4m3.cuh"
+#include "sm100.cuh"
 
 namespace hils {
 namespace {
 
-template <int D>
-__device__ __forceinline__ void stage8(float *dst, const uint8_t *src, int rows, float scale)
+constexpr int kWarps = 4;      // 128 threads of up to 255 registers: two blocks an SM
+constexpr int kHeads = 8;      // heads a row of work covers
+constexpr int kMaxSlots = HILS_MAX_K + 1;
+
+__device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t a0, const uint32_t a1, const uint32_t a2,
+                                        const uint32_t a3, const uint32_t b0, const uint32_t b1)
 {
-    for (int e = threadIdx.x; e < rows * D / 4; e += blockDim.x) {
-        float v[4];
-        e4m3x4_to_float(__ldg(reinterpret_cast<const uint32_t *>(src) + e), v);
-        reinterpret_cast<float4 *>(dst)[e] = make_float4(v[0] * scale, v[1] * scale, v[2] * scale, v[3] * scale);
-    }
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-template <typename Tin, typename Tout, int D>
-__global__ void attend8_kernel(Dims p, const Tin *__restrict__ Q, const uint8_t *__restrict__ K8,
-                               const uint8_t *__restrict__ V8, const float *__restrict__ ks, const float *__restrict__ vs,
-                               const int32_t *__restrict__ sel_idx, const float *__restrict__ sel_score,
-                               Tout *__restrict__ O)
+__device__ __forceinline__ uint32_t movmatrix_t(uint32_t x)
 {
-    extern __shared__ __align__(16) unsigned char smem_raw[];
-    float *Ks = reinterpret_cast<float *>(smem_raw);
-    float *Vs = Ks + (size_t)p.C * D;
-    float *qsm = Vs + (size_t)p.C * D;                                       // [G][D]
-    float *wsm = qsm + (size_t)p.G * D;                                      // [G][k+1]
-    int *chunk = reinterpret_cast<int *>(wsm + (size_t)p.G * (p.k + 1));     // [k+1]
+    uint32_t y;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
+}
 
-    const int i = blockIdx.x;
+// volatile: the loads stay where the pipeline below issues them
+template <int W>
+struct Vec;
+template <>
+struct Vec<4> {
+    uint32_t w[4];
+    __device__ __forceinline__ void load(const uint8_t *p)
+    {
+        asm volatile("ld.global.nc.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "l"(p));
+    }
+    __device__ __forceinline__ void zero() { w[0] = w[1] = w[2] = w[3] = 0u; }
+};
+template <>
+struct Vec<2> {
+    uint32_t w[2];
+    __device__ __forceinline__ void load(const uint8_t *p)
+    {
+        asm volatile("ld.global.nc.v2.u32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "l"(p));
+    }
+    __device__ __forceinline__ void zero() { w[0] = w[1] = 0u; }
+};
+
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi)
+{
+    const __half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+
+__device__ __forceinline__ float2 unpack_f16(uint32_t v) { return __half22float2(*reinterpret_cast<const __half2 *>(&v)); }
+
+__device__ __forceinline__ uint32_t cluster_rank() { uint32_t r; asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r)); return r; }
+__device__ __forceinline__ void cluster_sync()
+{
+    asm volatile("barrier.cluster.arrive.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
+}
+__device__ __forceinline__ float ld_cluster(uint32_t addr, uint32_t rank)
+{
+    uint32_t a;
+    float v;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(addr), "r"(rank));
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(a) : "memory");
+    return v;
+}
+
+// The tiles of one sub-chunk of MT x 16 keys in registers.
+template <int D, int MT>
+struct KTile {
+    Vec<4> v[MT][2][D / 64];
+    // p: the sub-chunk's first row + this lane's column; keys from n_vis on are not read
+    __device__ __forceinline__ void load(const uint8_t *p, int r, int n_vis)
+    {
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int key = 16 * m + 8 * h + r;
+#pragma unroll
+                for (int s = 0; s < D / 64; ++s) {
+                    if (key < n_vis) v[m][h][s].load(p + (size_t)key * D + 64 * s);
+                    else v[m][h][s].zero();
+                }
+            }
+    }
+};
+
+template <int D, int MT>
+struct VTile {
+    Vec<D / 32> v[MT][4];
+    __device__ __forceinline__ void load(const uint8_t *p, int t, int n_vis)
+    {
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const int key = 16 * m + 2 * t + (q & 1) + 8 * (q >> 1);
+                if (key < n_vis) v[m][q].load(p + (size_t)key * D);
+                else v[m][q].zero();
+            }
+    }
+};
+
+template <typename Tin, typename Tout, int D, int C>
+__global__ void __launch_bounds__(32 * kWarps, 2)
+    attend8_kernel(Dims p, int cs, int hgs, const Tin *__restrict__ Q, const uint8_t *__restrict__ K8,
+                   const uint8_t *__restrict__ V8, const float *__restrict__ ks, const float *__restrict__ vs,
+                   const int32_t *__restrict__ sel_idx, const float *__restrict__ sel_score, Tout *__restrict__ O)
+{
+    constexpr bool QHL = sizeof(Tin) == 4, PHL = sizeof(Tout) == 4;
+    constexpr int SUB = C < 64 ? C : 64, NSUB = C / SUB, MT = SUB / 16, KS = D / 16, DT = D / 16;
+    __shared__ float s_part[kWarps][kHeads][D + 4];   // + 4: the eight head rows of a fragment store on distinct banks
+    __shared__ float s_w[kHeads][kMaxSlots];
+    __shared__ float s_top[kHeads];
+    __shared__ int s_chunk[kMaxSlots];
+
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, r = lane >> 2, t = lane & 3;
+    const int rank = cs > 1 ? (int)cluster_rank() : 0;
+    const int unit = blockIdx.x / cs, i = unit / hgs;
     const size_t bg = blockIdx.y;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int h0 = (unit % hgs) * kHeads, nh = min(p.G - h0, kHeads);
     const long long pos = (long long)p.q_offset + i;
-    const int ns = p.k + 1;
-    const size_t row = (bg * p.G + warp) * p.N + i;
+    const int ci = (int)(pos / C), ns = p.k + 1, nw = kWarps * cs, me = rank * kWarps + warp;
     const int32_t *si = sel_idx + (bg * p.N + i) * p.k;
-    for (int x = lane; x < D; x += 32) qsm[warp * D + x] = to_float(Q[row * D + x]) * p.scale;
-    for (int j = threadIdx.x; j < ns; j += blockDim.x) chunk[j] = (j < p.k) ? si[j] : (int)(pos / p.C);
+    const uint8_t *Kb = K8 + bg * (size_t)p.T * D + 16 * t;
+    const uint8_t *Vb = V8 + bg * (size_t)p.T * D + (D / 8) * r;
+
+    // this warp's slots are me, me + nw, ..; the first one's tiles are asked for before anything else
+    auto chunk_of = [&](int j) { return j < p.k ? __ldg(si + j) : j == p.k ? ci : -1; };
+    auto seen = [&](int c) { return (int)min((long long)C, pos - (long long)c * C + 1); };
+    KTile<D, MT> kt;
+    VTile<D, MT> vt;
+    int j = me;
+    int c = chunk_of(j);
+    while (c < 0 && j + nw < ns) { j += nw; c = chunk_of(j); }
+    int nv = 0;
+    if (c >= 0) {
+        nv = seen(c);
+        kt.load(Kb + (size_t)c * C * D, r, nv);
+        vt.load(Vb + (size_t)c * C * D, t, nv);
+    }
+
+    // the query rows: lane (r, t) holds head h0 + r at d = 64 s + 16 t .. + 15
+    uint32_t qh[KS][2], ql[QHL ? KS : 1][2];
+    float fq;   // scale log2(e) / the row's power of two, for head r
+    {
+        float x[D / 64][16], m = 0.f;
+        const Tin *qr = Q + ((bg * p.G + h0 + min(r, nh - 1)) * p.N + i) * D + 16 * t;
+#pragma unroll
+        for (int s = 0; s < D / 64; ++s) {
+            load8(qr + 64 * s, x[s]);
+            load8(qr + 64 * s + 8, x[s] + 8);
+#pragma unroll
+            for (int e = 0; e < 16; ++e) m = fmaxf(m, fabsf(x[s][e]));
+        }
+        m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
+        m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
+        const int sh = min(14 - ((int)(__float_as_uint(m) >> 23) - 127), 120);
+        const float f = exp2_int(sh);
+        fq = p.scale * 1.4426950408889634f * exp2_int(-sh);
+#pragma unroll
+        for (int s = 0; s < D / 64; ++s)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const float a = x[s][2 * e] * f, b = x[s][2 * e + 1] * f;
+                const uint32_t v = pack_f16(a, b);
+                qh[4 * s + e / 2][e & 1] = v;
+                if constexpr (QHL) {
+                    const float2 y = unpack_f16(v);
+                    ql[4 * s + e / 2][e & 1] = pack_f16(a - y.x, b - y.y);
+                }
+            }
+    }
+    // this lane's columns of the products are heads 2t and 2t + 1
+    const float fq0 = __shfl_sync(0xFFFFFFFFu, fq, 8 * t), fq1 = __shfl_sync(0xFFFFFFFFu, fq, 8 * t + 4);
+
+    // slot factors w_c vs_c over the row's largest, times 2^14; a slot without a chunk has no weight, whatever its score
+    for (int h = warp; h < kHeads; h += kWarps) {
+        float s[3], v[3], mx = -INFINITY, z = 0.f, top = 0.f;
+#pragma unroll
+        for (int u = 0; u < 3; ++u) {
+            const int jj = lane + 32 * u;
+            const int cc = chunk_of(jj);
+            s[u] = (cc >= 0 && h < nh) ? __ldg(sel_score + ((bg * p.G + h0 + h) * p.N + i) * ns + jj) : -INFINITY;
+            v[u] = cc >= 0 ? __ldg(vs + bg * p.nL + cc) : 0.f;
+            if (h == 0 && jj < ns) s_chunk[jj] = cc;
+            mx = fmaxf(mx, s[u]);
+        }
+        mx = warp_max(mx);
+#pragma unroll
+        for (int u = 0; u < 3; ++u) {
+            s[u] = (s[u] == -INFINITY) ? 0.f : expf(s[u] - mx);
+            z += s[u];
+        }
+        z = warp_sum(z);
+        const float iz = z == 0.f ? 0.f : 1.0f / z;
+#pragma unroll
+        for (int u = 0; u < 3; ++u) {
+            s[u] = s[u] == 0.f ? 0.f : s[u] * iz * v[u];
+            top = fmaxf(top, fabsf(s[u]));
+        }
+        top = warp_max(top);
+        const float f = top > 0.f ? 16384.0f / top : 1.0f;
+#pragma unroll
+        for (int u = 0; u < 3; ++u)
+            if (lane + 32 * u < ns) s_w[h][lane + 32 * u] = s[u] * f;
+        if (lane == 0) s_top[h] = top > 0.f ? top * (1.0f / 16384.0f) : 0.f;
+    }
     __syncthreads();
-    // fusion weights; a slot without a chunk has no weight, whatever its score
-    float mx = -INFINITY, z = 0.f;
-    for (int j = lane; j < ns; j += 32) mx = fmaxf(mx, chunk[j] < 0 ? -INFINITY : sel_score[row * ns + j]);
-    mx = warp_max(mx);
-    for (int j = lane; j < ns; j += 32) {
-        const float s = chunk[j] < 0 ? -INFINITY : sel_score[row * ns + j];
-        const float e = (s == -INFINITY) ? 0.f : expf(s - mx);
-        wsm[warp * ns + j] = e;
-        z += e;
-    }
-    z = warp_sum(z);
-    const float inv = z > 0.f ? 1.0f / z : (z == 0.f ? 0.f : z);             // no weight at all: a zero row; NaN stays
-    float acc[D / 32];
+
+    float oacc[DT][4];
 #pragma unroll
-    for (int x = 0; x < D / 32; ++x) acc[x] = 0.f;
-    for (int j = 0; j < ns; ++j) {
-        const int c = chunk[j];
-        if (c < 0) continue;
-        const int n_vis = (int)min((long long)p.C, pos - (long long)c * p.C + 1);
-        const size_t at = (bg * p.T + (size_t)c * p.C) * D;
-        __syncthreads();
-        stage8<D>(Ks, K8 + at, n_vis, ks[bg * p.nL + c]);
-        stage8<D>(Vs, V8 + at, n_vis, vs[bg * p.nL + c]);
-        __syncthreads();
-        warp_attend_chunk<float, D>(qsm + warp * D, Ks, Vs, n_vis, wsm[warp * ns + j] * inv, acc);
-    }
+    for (int a = 0; a < DT; ++a)
 #pragma unroll
-    for (int x = 0; x < D / 32; ++x) store_out(O + row * D + lane * (D / 32) + x, acc[x]);
+        for (int e = 0; e < 4; ++e) oacc[a][e] = 0.f;
+
+    while (c >= 0) {
+        // the next slot of this warp that holds a chunk
+        int jn = j, cn = -1;
+        while (cn < 0 && jn + nw < ns) { jn += nw; cn = s_chunk[jn]; }
+        const int nvn = cn >= 0 ? seen(cn) : 0;
+        const float kc = __ldg(ks + bg * p.nL + c);
+        const float f0 = fq0 * kc, f1 = fq1 * kc;
+
+        // scores
+        float sacc[NSUB * MT][4];
+#pragma unroll
+        for (int sb = 0; sb < NSUB; ++sb) {
+#pragma unroll
+            for (int m = 0; m < MT; ++m) {
+                float(&d)[4] = sacc[sb * MT + m];
+                d[0] = d[1] = d[2] = d[3] = 0.f;
+#pragma unroll
+                for (int kk = 0; kk < KS; ++kk) {
+                    const uint32_t w0 = kt.v[m][0][kk >> 2].w[kk & 3], w1 = kt.v[m][1][kk >> 2].w[kk & 3];
+                    const uint32_t a0 = e4m3x2_to_f16x2(w0), a1 = e4m3x2_to_f16x2(w1);
+                    const uint32_t a2 = e4m3x2_to_f16x2(w0 >> 16), a3 = e4m3x2_to_f16x2(w1 >> 16);
+                    mma_f16(d, a0, a1, a2, a3, qh[kk][0], qh[kk][1]);
+                    if constexpr (QHL) mma_f16(d, a0, a1, a2, a3, ql[kk][0], ql[kk][1]);
+                }
+            }
+            if (sb + 1 < NSUB) kt.load(Kb + ((size_t)c * C + (sb + 1) * SUB) * D, r, nv - (sb + 1) * SUB);
+            else if (cn >= 0) kt.load(Kb + (size_t)cn * C * D, r, nvn);
+        }
+
+        // softmax over the keys seen (rows r, r + 8 of each tile, then across the lanes of a column)
+        float m0 = -INFINITY, m1 = -INFINITY;
+#pragma unroll
+        for (int m = 0; m < NSUB * MT; ++m)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                if (16 * m + 8 * h + r < nv) {
+                    m0 = fmaxf(m0, sacc[m][2 * h] * f0);
+                    m1 = fmaxf(m1, sacc[m][2 * h + 1] * f1);
+                }
+            }
+#pragma unroll
+        for (int o = 4; o < 32; o <<= 1) {
+            m0 = fmaxf(m0, __shfl_xor_sync(0xFFFFFFFFu, m0, o));
+            m1 = fmaxf(m1, __shfl_xor_sync(0xFFFFFFFFu, m1, o));
+        }
+        float l0 = 0.f, l1 = 0.f;
+#pragma unroll
+        for (int m = 0; m < NSUB * MT; ++m)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const bool in = 16 * m + 8 * h + r < nv;
+                const float e0 = in ? exp2f(fmaf(sacc[m][2 * h], f0, -m0)) : 0.f;
+                const float e1 = in ? exp2f(fmaf(sacc[m][2 * h + 1], f1, -m1)) : 0.f;
+                sacc[m][2 * h] = e0;
+                sacc[m][2 * h + 1] = e1;
+                l0 += e0;
+                l1 += e1;
+            }
+#pragma unroll
+        for (int o = 4; o < 32; o <<= 1) {
+            l0 += __shfl_xor_sync(0xFFFFFFFFu, l0, o);
+            l1 += __shfl_xor_sync(0xFFFFFFFFu, l1, o);
+        }
+        const float g0 = s_w[2 * t][j] / l0, g1 = s_w[2 * t + 1][j] / l1;
+
+        // values
+#pragma unroll
+        for (int sb = 0; sb < NSUB; ++sb) {
+#pragma unroll
+            for (int m = 0; m < MT; ++m) {
+                const float(&e)[4] = sacc[sb * MT + m];
+                const float x0 = e[0] * g0, x1 = e[1] * g1, x2 = e[2] * g0, x3 = e[3] * g1;
+                const uint32_t pa = pack_f16(x0, x1), pb = pack_f16(x2, x3);
+                const uint32_t b0 = movmatrix_t(pa), b1 = movmatrix_t(pb);
+                uint32_t c0 = 0u, c1 = 0u;
+                if constexpr (PHL) {
+                    const float2 ya = unpack_f16(pa), yb = unpack_f16(pb);
+                    c0 = movmatrix_t(pack_f16(x0 - ya.x, x1 - ya.y));
+                    c1 = movmatrix_t(pack_f16(x2 - yb.x, x3 - yb.y));
+                }
+#pragma unroll
+                for (int w = 0; w < D / 32; ++w) {
+                    const uint32_t k0 = vt.v[m][0].w[w], k1 = vt.v[m][1].w[w], k8 = vt.v[m][2].w[w], k9 = vt.v[m][3].w[w];
+#pragma unroll
+                    for (int hw = 0; hw < 2; ++hw) {
+                        const uint32_t lo = __byte_perm(k0, k1, hw ? 0x7362 : 0x5140);
+                        const uint32_t hi = __byte_perm(k8, k9, hw ? 0x7362 : 0x5140);
+                        const uint32_t a0 = e4m3x2_to_f16x2(lo), a1 = e4m3x2_to_f16x2(lo >> 16);
+                        const uint32_t a2 = e4m3x2_to_f16x2(hi), a3 = e4m3x2_to_f16x2(hi >> 16);
+                        mma_f16(oacc[2 * w + hw], a0, a1, a2, a3, b0, b1);
+                        if constexpr (PHL) mma_f16(oacc[2 * w + hw], a0, a1, a2, a3, c0, c1);
+                    }
+                }
+            }
+            if (sb + 1 < NSUB) vt.load(Vb + ((size_t)c * C + (sb + 1) * SUB) * D, t, nv - (sb + 1) * SUB);
+            else if (cn >= 0) vt.load(Vb + (size_t)cn * C * D, t, nvn);
+        }
+        j = jn;
+        c = cn;
+        nv = nvn;
+    }
+
+    // the warps' rows meet: tile a, row r is d = (D / 8) r + 2 a, row r + 8 the next one; columns are heads 2t, 2t + 1
+#pragma unroll
+    for (int a = 0; a < DT; ++a) {
+        const int x = (D / 8) * r + 2 * a;
+        *reinterpret_cast<float2 *>(&s_part[warp][2 * t][x]) = make_float2(oacc[a][0], oacc[a][2]);
+        *reinterpret_cast<float2 *>(&s_part[warp][2 * t + 1][x]) = make_float2(oacc[a][1], oacc[a][3]);
+    }
+    __syncthreads();
+    if (cs > 1) {
+        for (int e = tid; e < nh * D; e += 32 * kWarps) {
+            const int h = e / D, x = e % D;
+            float a = s_part[0][h][x];
+#pragma unroll
+            for (int w = 1; w < kWarps; ++w) a += s_part[w][h][x];
+            s_part[0][h][x] = a;
+        }
+        cluster_sync();
+        for (int e = rank * 32 * kWarps + tid; e < nh * D; e += cs * 32 * kWarps) {
+            const int h = e / D, x = e % D;
+            const uint32_t addr = sm100::smem_addr(&s_part[0][h][x]);
+            float a = 0.f;
+            for (int k = 0; k < cs; ++k) a += ld_cluster(addr, (uint32_t)k);
+            store_out(O + ((bg * p.G + h0 + h) * p.N + i) * D + x, a * s_top[h]);
+        }
+        cluster_sync();   // the others' reads of this block's rows
+        return;
+    }
+    for (int e = tid; e < nh * D; e += 32 * kWarps) {
+        const int h = e / D, x = e % D;
+        float a = s_part[0][h][x];
+#pragma unroll
+        for (int w = 1; w < kWarps; ++w) a += s_part[w][h][x];
+        store_out(O + ((bg * p.G + h0 + h) * p.N + i) * D + x, a * s_top[h]);
+    }
 }
 
-template <typename Tin, typename Tout, int D>
+// Blocks a row of work is split over (a cluster): with few rows, as many as the GPU's block slots (two an SM) hold at
+// once, until every warp has a single chunk.  More would queue behind the first ones, each paying its own start: 128 rows
+// of 33 slots take 36.9 us in single blocks, 28.7 in pairs (256 blocks), 36.9 in fours and 54 in eights; 8 rows of 65
+// slots 50, 30.8, 20.5 and 14.9.
+int split_of(const Dims &p, int hgs)
+{
+    const long long rows = (long long)p.B * p.Hkv * hgs * p.N;
+    int cs = 1;
+    while (cs < 8 && rows * cs * 2 <= 2 * 148 && cs * kWarps < p.k + 1) cs *= 2;
+    return cs;
+}
+
+template <typename Tin, typename Tout, int D, int C>
 cudaError_t launch_t(const Dims &p, const void *Q, const uint8_t *K8, const uint8_t *V8, const float *ks, const float *vs,
                      const int32_t *sel_idx, const float *sel_score, void *O, cudaStream_t s)
 {
-    const int ns = p.k + 1;
-    const size_t smem = (2 * (size_t)p.C * D + (size_t)p.G * D + (size_t)p.G * ns + ns) * 4;
-    auto kern = attend8_kernel<Tin, Tout, D>;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (e != cudaSuccess) return e;
-    kern<<<dim3(p.N, p.B * p.Hkv), 32 * p.G, smem, s>>>(p, static_cast<const Tin *>(Q), K8, V8, ks, vs, sel_idx, sel_score,
-                                                        static_cast<Tout *>(O));
-    return cudaGetLastError();
+    const int hgs = (p.G + kHeads - 1) / kHeads;
+    const int cs = split_of(p, hgs);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)((long long)p.N * hgs * cs), (unsigned)(p.B * p.Hkv));
+    cfg.blockDim = dim3(32 * kWarps);
+    cfg.stream = s;
+    cudaLaunchAttribute at;
+    at.id = cudaLaunchAttributeClusterDimension;
+    at.val.clusterDim.x = (unsigned)cs;
+    at.val.clusterDim.y = at.val.clusterDim.z = 1;
+    cfg.attrs = &at;
+    cfg.numAttrs = cs > 1 ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, attend8_kernel<Tin, Tout, D, C>, p, cs, hgs, static_cast<const Tin *>(Q), K8, V8, ks, vs,
+                              sel_idx, sel_score, static_cast<Tout *>(O));
+}
+
+template <typename Tin, typename Tout>
+cudaError_t launch_d(const Dims &p, const void *Q, const uint8_t *K8, const uint8_t *V8, const float *ks, const float *vs,
+                     const int32_t *sel_idx, const float *sel_score, void *O, cudaStream_t s)
+{
+    auto go = [&](auto f32, auto f64, auto f128) {
+        return (p.C == 32 ? f32 : p.C == 64 ? f64 : f128)(p, Q, K8, V8, ks, vs, sel_idx, sel_score, O, s);
+    };
+    return p.d == 64 ? go(launch_t<Tin, Tout, 64, 32>, launch_t<Tin, Tout, 64, 64>, launch_t<Tin, Tout, 64, 128>)
+                     : go(launch_t<Tin, Tout, 128, 32>, launch_t<Tin, Tout, 128, 64>, launch_t<Tin, Tout, 128, 128>);
 }
 
 }  // namespace
@@ -98,15 +437,11 @@ cudaError_t launch_attend8(const Dims &p, hils_dtype in, hils_dtype out, const v
                            const uint8_t *V8, const float *ks, const float *vs, const int32_t *sel_idx,
                            const float *sel_score, void *O, void *, const DeviceCtl &, cudaStream_t s)
 {
-    auto run = [&](auto f64, auto f128) {
-        return p.d == 64 ? f64(p, Q, K8, V8, ks, vs, sel_idx, sel_score, O, s)
-                         : f128(p, Q, K8, V8, ks, vs, sel_idx, sel_score, O, s);
-    };
     if (in == HILS_F32)
-        return out == HILS_F32 ? run(launch_t<float, float, 64>, launch_t<float, float, 128>)
-                               : run(launch_t<float, __nv_bfloat16, 64>, launch_t<float, __nv_bfloat16, 128>);
-    return out == HILS_F32 ? run(launch_t<__nv_bfloat16, float, 64>, launch_t<__nv_bfloat16, float, 128>)
-                           : run(launch_t<__nv_bfloat16, __nv_bfloat16, 64>, launch_t<__nv_bfloat16, __nv_bfloat16, 128>);
+        return out == HILS_F32 ? launch_d<float, float>(p, Q, K8, V8, ks, vs, sel_idx, sel_score, O, s)
+                               : launch_d<float, __nv_bfloat16>(p, Q, K8, V8, ks, vs, sel_idx, sel_score, O, s);
+    return out == HILS_F32 ? launch_d<__nv_bfloat16, float>(p, Q, K8, V8, ks, vs, sel_idx, sel_score, O, s)
+                           : launch_d<__nv_bfloat16, __nv_bfloat16>(p, Q, K8, V8, ks, vs, sel_idx, sel_score, O, s);
 }
 
 }  // namespace hils
