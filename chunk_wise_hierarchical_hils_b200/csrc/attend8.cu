@@ -34,15 +34,14 @@
 namespace hils {
 namespace {
 
-constexpr int kWarps = 4;      // 128 threads of up to 255 registers: two blocks an SM
+constexpr int kWarps = 4;
 constexpr int kHeads = 8;      // heads a row of work covers
 constexpr int kMaxSlots = HILS_MAX_K + 1;
 
 __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t a0, const uint32_t a1, const uint32_t a2,
                                         const uint32_t a3, const uint32_t b0, const uint32_t b1)
 {
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
@@ -50,31 +49,19 @@ __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t a0, const 
 __device__ __forceinline__ uint32_t movmatrix_t(uint32_t x)
 {
     uint32_t y;
-    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
     return y;
 }
 
 // volatile: the loads stay where the pipeline below issues them
-template <int W>
-struct Vec;
-template <>
-struct Vec<4> {
-    uint32_t w[4];
-    __device__ __forceinline__ void load(const uint8_t *p)
-    {
-        asm volatile("ld.global.nc.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "l"(p));
-    }
-    __device__ __forceinline__ void zero() { w[0] = w[1] = w[2] = w[3] = 0u; }
-};
-template <>
-struct Vec<2> {
-    uint32_t w[2];
-    __device__ __forceinline__ void load(const uint8_t *p)
-    {
-        asm volatile("ld.global.nc.v2.u32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "l"(p));
-    }
-    __device__ __forceinline__ void zero() { w[0] = w[1] = 0u; }
-};
+__device__ __forceinline__ void ldg16(uint32_t *w, const uint8_t *p)
+{
+    asm volatile("ld.global.nc.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "l"(p));
+}
+__device__ __forceinline__ void ldg8(uint32_t *w, const uint8_t *p)
+{
+    asm volatile("ld.global.nc.v2.u32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "l"(p));
+}
 
 __device__ __forceinline__ uint32_t pack_f16(float lo, float hi)
 {
@@ -98,51 +85,57 @@ __device__ __forceinline__ float ld_cluster(uint32_t addr, uint32_t rank)
     return v;
 }
 
-// The tiles of one sub-chunk of MT x 16 keys in registers.
-template <int D, int MT>
-struct KTile {
-    Vec<4> v[MT][2][D / 64];
-    // p: the sub-chunk's first row + this lane's column; keys from n_vis on are not read
-    __device__ __forceinline__ void load(const uint8_t *p, int r, int n_vis)
-    {
+// One tile of 16 keys in registers, D / 8 words a lane.  Keys: [2 rows][D / 64 segments][4 words]; values:
+// [4 keys][D / 32 words].  p: the tile's first row + this lane's column; left: the keys of the tile that may be read
+// (16 or more: all of them; the same for the whole warp).
+template <int D>
+__device__ __forceinline__ void load_k(uint32_t *w, const uint8_t *p, int r, int left)
+{
+    if (left >= 16) {
 #pragma unroll
-        for (int m = 0; m < MT; ++m)
+        for (int h = 0; h < 2; ++h)
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const int key = 16 * m + 8 * h + r;
-#pragma unroll
-                for (int s = 0; s < D / 64; ++s) {
-                    if (key < n_vis) v[m][h][s].load(p + (size_t)key * D + 64 * s);
-                    else v[m][h][s].zero();
-                }
-            }
+            for (int s = 0; s < D / 64; ++s) ldg16(w + (h * (D / 64) + s) * 4, p + (8 * h + r) * D + 64 * s);
+        return;
     }
-};
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int s = 0; s < D / 64; ++s) {
+            uint32_t *x = w + (h * (D / 64) + s) * 4;
+            if (8 * h + r < left) ldg16(x, p + (8 * h + r) * D + 64 * s);
+            else x[0] = x[1] = x[2] = x[3] = 0u;
+        }
+}
 
-template <int D, int MT>
-struct VTile {
-    Vec<D / 32> v[MT][4];
-    __device__ __forceinline__ void load(const uint8_t *p, int t, int n_vis)
-    {
+template <int D>
+__device__ __forceinline__ void load_v(uint32_t *w, const uint8_t *p, int t, int left)
+{
+    constexpr int W = D / 32;
 #pragma unroll
-        for (int m = 0; m < MT; ++m)
+    for (int q = 0; q < 4; ++q) {
+        const int key = 2 * t + (q & 1) + 8 * (q >> 1);
+        if (left >= 16 || key < left) {
+            if constexpr (W == 4) ldg16(w + q * W, p + key * D);
+            else ldg8(w + q * W, p + key * D);
+        } else {
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                const int key = 16 * m + 2 * t + (q & 1) + 8 * (q >> 1);
-                if (key < n_vis) v[m][q].load(p + (size_t)key * D);
-                else v[m][q].zero();
-            }
+            for (int x = 0; x < W; ++x) w[q * W + x] = 0u;
+        }
     }
-};
+}
+
+// Blocks an SM holds, by the registers a thread needs.
+constexpr int blocks_per_sm(int D, int C, bool wide_q) { return D == 64 ? 4 : (C == 128 || wide_q) ? 2 : 3; }
 
 template <typename Tin, typename Tout, int D, int C>
-__global__ void __launch_bounds__(32 * kWarps, 2)
+__global__ void __launch_bounds__(32 * kWarps, blocks_per_sm(D, C, sizeof(Tin) == 4))
     attend8_kernel(Dims p, int cs, int hgs, const Tin *__restrict__ Q, const uint8_t *__restrict__ K8,
                    const uint8_t *__restrict__ V8, const float *__restrict__ ks, const float *__restrict__ vs,
                    const int32_t *__restrict__ sel_idx, const float *__restrict__ sel_score, Tout *__restrict__ O)
 {
     constexpr bool QHL = sizeof(Tin) == 4, PHL = sizeof(Tout) == 4;
-    constexpr int SUB = C < 64 ? C : 64, NSUB = C / SUB, MT = SUB / 16, KS = D / 16, DT = D / 16;
+    constexpr int MT = C / 16, KS = D / 16, DT = D / 16, WORDS = D / 8;
     __shared__ float s_part[kWarps][kHeads][D + 4];   // + 4: the eight head rows of a fragment store on distinct banks
     __shared__ float s_w[kHeads][kMaxSlots];
     __shared__ float s_top[kHeads];
@@ -159,19 +152,25 @@ __global__ void __launch_bounds__(32 * kWarps, 2)
     const uint8_t *Kb = K8 + bg * (size_t)p.T * D + 16 * t;
     const uint8_t *Vb = V8 + bg * (size_t)p.T * D + (D / 8) * r;
 
+    // A chunk is a stream of 2 MT tiles, its keys' and then its values', through four register buffers: once tile n
+    // is used, its buffer is loaded with tile n + 4 of the stream, which runs on into the warp's next chunk.
+    uint32_t buf[4][WORDS];
+    auto load_tile = [&](int n, int c, int left) {   // tile n of chunk c, of which `left` keys are seen
+        if (n < MT) load_k<D>(buf[n & 3], Kb + ((size_t)c * C + 16 * n) * D, r, left - 16 * n);
+        else load_v<D>(buf[n & 3], Vb + ((size_t)c * C + 16 * (n - MT)) * D, t, left - 16 * (n - MT));
+    };
+
     // this warp's slots are me, me + nw, ..; the first one's tiles are asked for before anything else
     auto chunk_of = [&](int j) { return j < p.k ? __ldg(si + j) : j == p.k ? ci : -1; };
     auto seen = [&](int c) { return (int)min((long long)C, pos - (long long)c * C + 1); };
-    KTile<D, MT> kt;
-    VTile<D, MT> vt;
     int j = me;
     int c = chunk_of(j);
     while (c < 0 && j + nw < ns) { j += nw; c = chunk_of(j); }
     int nv = 0;
     if (c >= 0) {
         nv = seen(c);
-        kt.load(Kb + (size_t)c * C * D, r, nv);
-        vt.load(Vb + (size_t)c * C * D, t, nv);
+#pragma unroll
+        for (int n = 0; n < 4; ++n) load_tile(n, c, nv);
     }
 
     // the query rows: lane (r, t) holds head h0 + r at d = 64 s + 16 t .. + 15
@@ -256,31 +255,36 @@ __global__ void __launch_bounds__(32 * kWarps, 2)
         const float kc = __ldg(ks + bg * p.nL + c);
         const float f0 = fq0 * kc, f1 = fq1 * kc;
 
-        // scores
-        float sacc[NSUB * MT][4];
+        // scores, two tiles of keys at a time: their products are independent of one another
+        float sacc[MT][4];
 #pragma unroll
-        for (int sb = 0; sb < NSUB; ++sb) {
+        for (int m = 0; m < MT; m += 2) {
 #pragma unroll
-            for (int m = 0; m < MT; ++m) {
-                float(&d)[4] = sacc[sb * MT + m];
-                d[0] = d[1] = d[2] = d[3] = 0.f;
+            for (int e = 0; e < 4; ++e) sacc[m][e] = sacc[m + 1][e] = 0.f;
 #pragma unroll
-                for (int kk = 0; kk < KS; ++kk) {
-                    const uint32_t w0 = kt.v[m][0][kk >> 2].w[kk & 3], w1 = kt.v[m][1][kk >> 2].w[kk & 3];
+            for (int kk = 0; kk < KS; ++kk) {
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    const uint32_t *w = buf[(m + u) & 3];
+                    const uint32_t w0 = w[kk], w1 = w[KS + kk];
                     const uint32_t a0 = e4m3x2_to_f16x2(w0), a1 = e4m3x2_to_f16x2(w1);
                     const uint32_t a2 = e4m3x2_to_f16x2(w0 >> 16), a3 = e4m3x2_to_f16x2(w1 >> 16);
-                    mma_f16(d, a0, a1, a2, a3, qh[kk][0], qh[kk][1]);
-                    if constexpr (QHL) mma_f16(d, a0, a1, a2, a3, ql[kk][0], ql[kk][1]);
+                    mma_f16(sacc[m + u], a0, a1, a2, a3, qh[kk][0], qh[kk][1]);
+                    if constexpr (QHL) mma_f16(sacc[m + u], a0, a1, a2, a3, ql[kk][0], ql[kk][1]);
                 }
             }
-            if (sb + 1 < NSUB) kt.load(Kb + ((size_t)c * C + (sb + 1) * SUB) * D, r, nv - (sb + 1) * SUB);
-            else if (cn >= 0) kt.load(Kb + (size_t)cn * C * D, r, nvn);
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                const int n = m + u + 4;
+                if (n < 2 * MT) load_tile(n, c, nv);
+                else if (cn >= 0) load_tile(n - 2 * MT, cn, nvn);
+            }
         }
 
         // softmax over the keys seen (rows r, r + 8 of each tile, then across the lanes of a column)
         float m0 = -INFINITY, m1 = -INFINITY;
 #pragma unroll
-        for (int m = 0; m < NSUB * MT; ++m)
+        for (int m = 0; m < MT; ++m)
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 if (16 * m + 8 * h + r < nv) {
@@ -295,7 +299,7 @@ __global__ void __launch_bounds__(32 * kWarps, 2)
         }
         float l0 = 0.f, l1 = 0.f;
 #pragma unroll
-        for (int m = 0; m < NSUB * MT; ++m)
+        for (int m = 0; m < MT; ++m)
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 const bool in = 16 * m + 8 * h + r < nv;
@@ -315,35 +319,34 @@ __global__ void __launch_bounds__(32 * kWarps, 2)
 
         // values
 #pragma unroll
-        for (int sb = 0; sb < NSUB; ++sb) {
+        for (int m = 0; m < MT; ++m) {
+            const float(&e)[4] = sacc[m];
+            const uint32_t *vw = buf[(MT + m) & 3];
+            const float x0 = e[0] * g0, x1 = e[1] * g1, x2 = e[2] * g0, x3 = e[3] * g1;
+            const uint32_t pa = pack_f16(x0, x1), pb = pack_f16(x2, x3);
+            const uint32_t b0 = movmatrix_t(pa), b1 = movmatrix_t(pb);
+            uint32_t c0 = 0u, c1 = 0u;
+            if constexpr (PHL) {
+                const float2 ya = unpack_f16(pa), yb = unpack_f16(pb);
+                c0 = movmatrix_t(pack_f16(x0 - ya.x, x1 - ya.y));
+                c1 = movmatrix_t(pack_f16(x2 - yb.x, x3 - yb.y));
+            }
 #pragma unroll
-            for (int m = 0; m < MT; ++m) {
-                const float(&e)[4] = sacc[sb * MT + m];
-                const float x0 = e[0] * g0, x1 = e[1] * g1, x2 = e[2] * g0, x3 = e[3] * g1;
-                const uint32_t pa = pack_f16(x0, x1), pb = pack_f16(x2, x3);
-                const uint32_t b0 = movmatrix_t(pa), b1 = movmatrix_t(pb);
-                uint32_t c0 = 0u, c1 = 0u;
-                if constexpr (PHL) {
-                    const float2 ya = unpack_f16(pa), yb = unpack_f16(pb);
-                    c0 = movmatrix_t(pack_f16(x0 - ya.x, x1 - ya.y));
-                    c1 = movmatrix_t(pack_f16(x2 - yb.x, x3 - yb.y));
-                }
+            for (int w = 0; w < D / 32; ++w) {
+                const uint32_t k0 = vw[w], k1 = vw[D / 32 + w], k8 = vw[2 * (D / 32) + w], k9 = vw[3 * (D / 32) + w];
 #pragma unroll
-                for (int w = 0; w < D / 32; ++w) {
-                    const uint32_t k0 = vt.v[m][0].w[w], k1 = vt.v[m][1].w[w], k8 = vt.v[m][2].w[w], k9 = vt.v[m][3].w[w];
-#pragma unroll
-                    for (int hw = 0; hw < 2; ++hw) {
-                        const uint32_t lo = __byte_perm(k0, k1, hw ? 0x7362 : 0x5140);
-                        const uint32_t hi = __byte_perm(k8, k9, hw ? 0x7362 : 0x5140);
-                        const uint32_t a0 = e4m3x2_to_f16x2(lo), a1 = e4m3x2_to_f16x2(lo >> 16);
-                        const uint32_t a2 = e4m3x2_to_f16x2(hi), a3 = e4m3x2_to_f16x2(hi >> 16);
-                        mma_f16(oacc[2 * w + hw], a0, a1, a2, a3, b0, b1);
-                        if constexpr (PHL) mma_f16(oacc[2 * w + hw], a0, a1, a2, a3, c0, c1);
-                    }
+                for (int hw = 0; hw < 2; ++hw) {
+                    const uint32_t lo = __byte_perm(k0, k1, hw ? 0x7362 : 0x5140);
+                    const uint32_t hi = __byte_perm(k8, k9, hw ? 0x7362 : 0x5140);
+                    const uint32_t a0 = e4m3x2_to_f16x2(lo), a1 = e4m3x2_to_f16x2(lo >> 16);
+                    const uint32_t a2 = e4m3x2_to_f16x2(hi), a3 = e4m3x2_to_f16x2(hi >> 16);
+                    mma_f16(oacc[2 * w + hw], a0, a1, a2, a3, b0, b1);
+                    if constexpr (PHL) mma_f16(oacc[2 * w + hw], a0, a1, a2, a3, c0, c1);
                 }
             }
-            if (sb + 1 < NSUB) vt.load(Vb + ((size_t)c * C + (sb + 1) * SUB) * D, t, nv - (sb + 1) * SUB);
-            else if (cn >= 0) vt.load(Vb + (size_t)cn * C * D, t, nvn);
+            const int n = MT + m + 4;
+            if (n < 2 * MT) load_tile(n, c, nv);
+            else if (cn >= 0) load_tile(n - 2 * MT, cn, nvn);
         }
         j = jn;
         c = cn;
@@ -386,16 +389,16 @@ __global__ void __launch_bounds__(32 * kWarps, 2)
     }
 }
 
-// Blocks a row of work is split over (a cluster): with few rows, as many as the GPU's block slots (two an SM) hold at
-// once, until every warp has a single chunk.  More would queue behind the first ones, each paying its own start: 128 rows
-// of 33 slots take 36.9 us in single blocks, 28.7 in pairs (256 blocks), 36.9 in fours and 54 in eights; 8 rows of 65
-// slots 50, 30.8, 20.5 and 14.9.
-int split_of(const Dims &p, int hgs)
+// Blocks a row of work is split over (a cluster of up to 8): as many as the GPU holds at once, more would queue
+// behind the first ones; and no more than shorten the longest warp's list of chunks.
+int split_of(const Dims &p, int hgs, int per_sm)
 {
-    const long long rows = (long long)p.B * p.Hkv * hgs * p.N;
-    int cs = 1;
-    while (cs < 8 && rows * cs * 2 <= 2 * 148 && cs * kWarps < p.k + 1) cs *= 2;
-    return cs;
+    const long long rows = (long long)p.B * p.Hkv * hgs * p.N, slots = 148ll * per_sm;
+    int best = 1;
+    auto rounds = [&](int cs) { return (p.k + kWarps * cs) / (kWarps * cs); };
+    for (int cs = 2; cs <= 8 && rows * cs <= slots; ++cs)
+        if (rounds(cs) < rounds(best)) best = cs;
+    return best;
 }
 
 template <typename Tin, typename Tout, int D, int C>
@@ -403,7 +406,7 @@ cudaError_t launch_t(const Dims &p, const void *Q, const uint8_t *K8, const uint
                      const int32_t *sel_idx, const float *sel_score, void *O, cudaStream_t s)
 {
     const int hgs = (p.G + kHeads - 1) / kHeads;
-    const int cs = split_of(p, hgs);
+    const int cs = split_of(p, hgs, blocks_per_sm(D, C, sizeof(Tin) == 4));
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)((long long)p.N * hgs * cs), (unsigned)(p.B * p.Hkv));
     cfg.blockDim = dim3(32 * kWarps);
