@@ -28,48 +28,17 @@
 // memory (distributed shared memory for a cluster): no workspace, no atomics, a fixed order.
 #include "attend_simt.cuh"
 #include "cache8.h"
-#include "e4m3.cuh"
 #include "sm100.cuh"
+#include "tiles8.cuh"
 
 namespace hils {
 namespace {
 
+using namespace t8;
+
 constexpr int kWarps = 4;
 constexpr int kHeads = 8;      // heads a row of work covers
 constexpr int kMaxSlots = HILS_MAX_K + 1;
-
-__device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t a0, const uint32_t a1, const uint32_t a2,
-                                        const uint32_t a3, const uint32_t b0, const uint32_t b1)
-{
-    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
-        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-
-__device__ __forceinline__ uint32_t movmatrix_t(uint32_t x)
-{
-    uint32_t y;
-    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
-    return y;
-}
-
-// volatile: the loads stay where the pipeline below issues them
-__device__ __forceinline__ void ldg16(uint32_t *w, const uint8_t *p)
-{
-    asm volatile("ld.global.nc.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "l"(p));
-}
-__device__ __forceinline__ void ldg8(uint32_t *w, const uint8_t *p)
-{
-    asm volatile("ld.global.nc.v2.u32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "l"(p));
-}
-
-__device__ __forceinline__ uint32_t pack_f16(float lo, float hi)
-{
-    const __half2 h = __floats2half2_rn(lo, hi);
-    return *reinterpret_cast<const uint32_t *>(&h);
-}
-
-__device__ __forceinline__ float2 unpack_f16(uint32_t v) { return __half22float2(*reinterpret_cast<const __half2 *>(&v)); }
 
 __device__ __forceinline__ uint32_t cluster_rank() { uint32_t r; asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r)); return r; }
 __device__ __forceinline__ void cluster_sync()
@@ -83,46 +52,6 @@ __device__ __forceinline__ float ld_cluster(uint32_t addr, uint32_t rank)
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(addr), "r"(rank));
     asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(a) : "memory");
     return v;
-}
-
-// One tile of 16 keys in registers, D / 8 words a lane.  Keys: [2 rows][D / 64 segments][4 words]; values:
-// [4 keys][D / 32 words].  p: the tile's first row + this lane's column; left: the keys of the tile that may be read
-// (16 or more: all of them; the same for the whole warp).
-template <int D>
-__device__ __forceinline__ void load_k(uint32_t *w, const uint8_t *p, int r, int left)
-{
-    if (left >= 16) {
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-#pragma unroll
-            for (int s = 0; s < D / 64; ++s) ldg16(w + (h * (D / 64) + s) * 4, p + (8 * h + r) * D + 64 * s);
-        return;
-    }
-#pragma unroll
-    for (int h = 0; h < 2; ++h)
-#pragma unroll
-        for (int s = 0; s < D / 64; ++s) {
-            uint32_t *x = w + (h * (D / 64) + s) * 4;
-            if (8 * h + r < left) ldg16(x, p + (8 * h + r) * D + 64 * s);
-            else x[0] = x[1] = x[2] = x[3] = 0u;
-        }
-}
-
-template <int D>
-__device__ __forceinline__ void load_v(uint32_t *w, const uint8_t *p, int t, int left)
-{
-    constexpr int W = D / 32;
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-        const int key = 2 * t + (q & 1) + 8 * (q >> 1);
-        if (left >= 16 || key < left) {
-            if constexpr (W == 4) ldg16(w + q * W, p + key * D);
-            else ldg8(w + q * W, p + key * D);
-        } else {
-#pragma unroll
-            for (int x = 0; x < W; ++x) w[q * W + x] = 0u;
-        }
-    }
 }
 
 // Blocks an SM holds, by the registers a thread needs.

@@ -1,0 +1,136 @@
+// tiles8.cuh -- register tiles of the 8-bit cache and their mma.sync products (sm_100a).
+//
+// A warp takes tiles of 16 rows (keys) straight from global memory into registers.  The index orders inside an mma product
+// are free, so rows and columns are permuted until what a lane's 16-byte loads bring is what its fragments hold; lane
+// (r, t) = (lane / 4, lane % 4):
+//   K tile   rows r and r + 8, bytes d = 64 s + 16 t + 0..15 (s < d / 64): the A fragments of a product over d
+//   V tile   rows 2t, 2t+1, 2t+8, 2t+9, bytes d = (d / 8) r + ..: after a byte transpose (four rows x four columns) the
+//            A fragments of a product over the rows
+#pragma once
+
+#include <cuda_fp16.h>
+#include <stdint.h>
+
+#include "e4m3.cuh"
+
+namespace hils {
+namespace t8 {
+
+// volatile: the loads stay where a kernel's pipeline issues them
+__device__ __forceinline__ void ldg16(uint32_t *w, const uint8_t *p)
+{
+    asm volatile("ld.global.nc.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "l"(p));
+}
+
+__device__ __forceinline__ void ldg8(uint32_t *w, const uint8_t *p)
+{
+    asm volatile("ld.global.nc.v2.u32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "l"(p));
+}
+
+// One tile, D / 8 words a lane.  Keys: [2 rows][D / 64 segments][4 words]; values: [4 rows][D / 32 words].
+// p: the tile's first row + this lane's column (16 t, or (D / 8) r); left: the rows of the tile that may be read (16 or
+// more: all of them; the same for the whole warp).  The others become zeros.
+template <int D>
+__device__ __forceinline__ void load_k(uint32_t *w, const uint8_t *p, int r, int left)
+{
+    if (left >= 16) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int s = 0; s < D / 64; ++s) ldg16(w + (h * (D / 64) + s) * 4, p + (8 * h + r) * D + 64 * s);
+        return;
+    }
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int s = 0; s < D / 64; ++s) {
+            uint32_t *x = w + (h * (D / 64) + s) * 4;
+            if (8 * h + r < left) ldg16(x, p + (8 * h + r) * D + 64 * s);
+            else x[0] = x[1] = x[2] = x[3] = 0u;
+        }
+}
+
+template <int D>
+__device__ __forceinline__ void load_v(uint32_t *w, const uint8_t *p, int t, int left)
+{
+    constexpr int W = D / 32;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+        const int key = 2 * t + (q & 1) + 8 * (q >> 1);
+        if (left >= 16 || key < left) {
+            if constexpr (W == 4) ldg16(w + q * W, p + key * D);
+            else ldg8(w + q * W, p + key * D);
+        } else {
+#pragma unroll
+            for (int x = 0; x < W; ++x) w[q * W + x] = 0u;
+        }
+    }
+}
+
+// D (16 x 8, f32) += A (16 x 16, f16) B (16 x 8)
+__device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                        uint32_t b1)
+{
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// D (16 x 8, f32) += A (16 x 32, e4m3) B (32 x 8): a quarter of the f16 product's cycles per element on B200 (4.6 against
+// 2 x 8 a warp), with float32 sums (errors of 2^-24 of the largest term measured)
+__device__ __forceinline__ void mma_e4m3(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1)
+{
+    asm("mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// 8 x 8 matrix of 16-bit elements, transposed across the warp
+__device__ __forceinline__ uint32_t movmatrix_t(uint32_t x)
+{
+    uint32_t y;
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
+}
+
+// Four rows of four bytes -> four columns: o[x] = byte x of a, b, c, d.
+__device__ __forceinline__ void transpose4(uint32_t a, uint32_t b, uint32_t c, uint32_t d, uint32_t (&o)[4])
+{
+    const uint32_t ab0 = __byte_perm(a, b, 0x5140), ab1 = __byte_perm(a, b, 0x7362);   // a0 b0 a1 b1, a2 b2 a3 b3
+    const uint32_t cd0 = __byte_perm(c, d, 0x5140), cd1 = __byte_perm(c, d, 0x7362);
+    o[0] = __byte_perm(ab0, cd0, 0x5410);
+    o[1] = __byte_perm(ab0, cd0, 0x7632);
+    o[2] = __byte_perm(ab1, cd1, 0x5410);
+    o[3] = __byte_perm(ab1, cd1, 0x7632);
+}
+
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi)
+{
+    const __half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+
+__device__ __forceinline__ float2 unpack_f16(uint32_t v) { return __half22float2(*reinterpret_cast<const __half2 *>(&v)); }
+
+// Two f16 values -> two e4m3 bytes (low 16 bits), nearest even.
+__device__ __forceinline__ uint32_t f16x2_to_e4m3x2(uint32_t h)
+{
+    uint16_t r;
+    asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(r) : "r"(h));
+    return r;
+}
+
+// What two e4m3 bytes leave of the two f16 values they round, times SCALE (16 or 1): exact in f16, the difference having
+// at most the value's bits below the top four.
+template <int SCALE>
+__device__ __forceinline__ uint32_t e4m3_rest(uint32_t h, uint32_t bytes)
+{
+    const uint32_t b = e4m3x2_to_f16x2(bytes);
+    __half2 d = __hsub2(*reinterpret_cast<const __half2 *>(&h), *reinterpret_cast<const __half2 *>(&b));
+    if constexpr (SCALE != 1) d = __hmul2(d, __float2half2_rn((float)SCALE));
+    return *reinterpret_cast<const uint32_t *>(&d);
+}
+
+}  // namespace t8
+}  // namespace hils
