@@ -11,8 +11,11 @@
 // values (for the sum; these loads hit L1), through four register buffers, running on into the warp's next chunk.
 //
 // Numbers.  The other operand, one row of u or p, is float32: it is split into pieces of e4m3's four bits, each 2^4 finer
-// than the one before, in the columns the product has anyway (column c holds piece c): six pieces hold 24 bits (u
-// relative to the row's largest, p relative to the chunk's largest).  The columns' sums meet in float32.
+// than the one before, in the columns the product has anyway (column c holds piece c).  For float32 results six pieces
+// hold 24 bits (u relative to the row's largest, p to the chunk's largest); for bf16 ones two pieces hold a bf16 u
+// and three the 11 bits of p (2^-12 of its value, where the result's own rounding is 2^-9).  The columns' sums meet in
+// float32.  A lane splits the values it holds and the pieces change places in shared memory: splitting the row in
+// every lane that needs one piece of it took three times the instructions (2129 a chunk against 750).
 #include "cache8.h"
 #include "common.cuh"
 #include "tiles8.cuh"
@@ -25,20 +28,39 @@ using namespace t8;
 constexpr int kWarps = 4;
 constexpr int kBlocksPerSm = 3;
 
-// Piece r (the lane's column) of the values a, b, both below 256 in magnitude, as two e4m3 bytes: 16^r times what
-// pieces 0..r-1 leave of them; no piece beyond the sixth.
-__device__ __forceinline__ uint32_t piece_pair(float a, float b, int r)
+// The pieces of two values below 256 in magnitude: o[c] holds the e4m3 bytes of 16^c times what pieces 0 .. c - 1 leave.
+template <int N>
+__device__ __forceinline__ void pieces(float a, float b, uint32_t (&o)[N])
 {
+    static_assert(N == 2 || N == 3 || N == 6, "pieces of one or two f16 values");
     uint32_t h = pack_f16(a, b);
-    if (r >= 3) {
-        const float2 y = unpack_f16(h);
-        h = pack_f16((a - y.x) * 4096.0f, (b - y.y) * 4096.0f);
+    const float2 y = unpack_f16(h);
+#pragma unroll
+    for (int c = 0; c < (N < 3 ? N : 3); ++c) {
+        o[c] = f16x2_to_e4m3x2(h);
+        h = e4m3_rest<16>(h, o[c]);
     }
-    const int q = r >= 3 ? r - 3 : r;
-    const uint32_t p0 = f16x2_to_e4m3x2(h), h1 = e4m3_rest<16>(h, p0);
-    const uint32_t p1 = f16x2_to_e4m3x2(h1), p2 = f16x2_to_e4m3x2(e4m3_rest<16>(h1, p1));
-    return r >= 6 ? 0u : q == 0 ? p0 : q == 1 ? p1 : p2;
+    if constexpr (N == 6) {
+        h = pack_f16((a - y.x) * 4096.0f, (b - y.y) * 4096.0f);
+#pragma unroll
+        for (int c = 3; c < 6; ++c) {
+            o[c] = f16x2_to_e4m3x2(h);
+            h = e4m3_rest<16>(h, o[c]);
+        }
+    }
 }
+
+// Four consecutive elements, raw until they are used.
+__device__ __forceinline__ void widen4(float4 v, float *o) { o[0] = v.x; o[1] = v.y; o[2] = v.z; o[3] = v.w; }
+__device__ __forceinline__ void widen4(uint2 v, float *o)
+{
+    o[0] = __uint_as_float(v.x << 16); o[1] = __uint_as_float(v.x & 0xFFFF0000u);
+    o[2] = __uint_as_float(v.y << 16); o[3] = __uint_as_float(v.y & 0xFFFF0000u);
+}
+template <typename T>
+struct Raw4 { typedef uint2 type; };
+template <>
+struct Raw4<float> { typedef float4 type; };
 
 __device__ __forceinline__ float sum_t(float x)   // over the four lanes of a row
 {
@@ -69,21 +91,33 @@ __global__ void __launch_bounds__(32 * kWarps, kBlocksPerSm)
                       Tin *__restrict__ L, float *__restrict__ beta, Cache8 p, float scale, int c0, int span, int t_end)
 {
     constexpr int MT = C / 16, KS = D / 32, DT = D / 16, WORDS = D / 8, W = D / 32;
-    const int lane = threadIdx.x & 31, r = lane >> 2, t = lane & 3;
-    const long long units = (long long)p.B * p.Hkv * span, step = (long long)gridDim.x * kWarps;
+    constexpr bool F32 = sizeof(Tin) == 4;
+    constexpr int NU = F32 ? 6 : 2, NP = F32 ? 6 : 3;   // pieces of u and of p
+    typedef typename Raw4<Tin>::type Raw;
+    // pieces on their way between lanes: u's as [word of the row][piece] (a word: four values), p's as [tile][piece][lane t]
+    __shared__ __align__(16) uint32_t s_u[kWarps][D / 4][8];
+    __shared__ uint32_t s_p[kWarps][MT][8][4];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = lane >> 2, t = lane & 3;
+    const unsigned units = (unsigned)(p.B * p.Hkv) * (unsigned)span, step = gridDim.x * kWarps;
     const float f0 = exp2_int(-8 * t), f1 = exp2_int(-8 * t - 4);   // worth of pieces 2t and 2t + 1
 
+    unsigned unit = blockIdx.x * kWarps + warp;
+    if (unit >= units) return;   // whole warps leave; no block barrier follows
+    for (int i = lane; i < D / 4 * 8; i += 32) (&s_u[warp][0][0])[i] = 0u;   // columns without a piece stay zero
+    for (int i = lane; i < MT * 32; i += 32) (&s_p[warp][0][0][0])[i] = 0u;
+
     struct At {
-        long long bg;
-        int c, rows;
+        size_t crow;
+        int rows;
         const uint8_t *row0;
     };
-    auto at = [&](long long u) {
+    auto at = [&](unsigned u) {
         At a;
-        a.bg = u / span;
-        a.c = c0 + (int)(u - a.bg * span);
-        a.rows = (int)min((long long)C, (long long)t_end - (long long)a.c * C);
-        a.row0 = K8 + ((size_t)a.bg * p.T + (size_t)a.c * C) * D;
+        const unsigned bg = u / (unsigned)span;
+        const int c = c0 + (int)(u - bg * (unsigned)span);
+        a.crow = (size_t)bg * p.nL + c;
+        a.rows = (int)min((long long)C, (long long)t_end - (long long)c * C);
+        a.row0 = K8 + ((size_t)bg * p.T + (size_t)c * C) * D;
         return a;
     };
     uint32_t buf[4][WORDS];
@@ -91,44 +125,40 @@ __global__ void __launch_bounds__(32 * kWarps, kBlocksPerSm)
         if (n < MT) load_k<D>(buf[n & 3], a.row0 + 16 * n * D + 16 * t, r, a.rows - 16 * n);
         else load_v<D>(buf[n & 3], a.row0 + 16 * (n - MT) * D + (D / 8) * r, t, a.rows - 16 * (n - MT));
     };
+    // the landmark query: lane (r, t) takes its word r of column block t (d = 64 (r / 4) + 16 t + 4 (r % 4))
+    const int ud = (64 * (r >> 2) + 16 * t + 4 * (r & 3)) % D;   // d = 64: lanes of r >= 4 repeat the others
+    auto load_u = [&](const At &a) { return *reinterpret_cast<const Raw *>(U + a.crow * D + ud); };
 
-    long long unit = (long long)blockIdx.x * kWarps + (threadIdx.x >> 5);
-    if (unit >= units) return;   // whole warps leave; no block barrier follows
     At a = at(unit);
 #pragma unroll
     for (int n = 0; n < 4; ++n) load_tile(n, a);
+    Raw ur = load_u(a);
+    float sc = __ldg(ks + a.crow);
     for (;;) {
-        const long long next = unit + step;
-        const bool more = next < units;
+        const bool more = units - unit > step;
         At an = a;
-        if (more) an = at(next);
-        const size_t crow = (size_t)a.bg * p.nL + a.c;
-        const float sc = __ldg(ks + crow);
+        if (more) an = at(unit + step);
 
         // the landmark query's pieces: lane (r, t) holds piece r at d = 64 s + 16 t .. + 15
         uint32_t ub[KS][2];
         float fu;
         {
-            float x[D / 64][16], m = 0.f;
-            const Tin *ur = U + crow * D + 16 * t;
-#pragma unroll
-            for (int s = 0; s < D / 64; ++s) {
-                load8(ur + 64 * s, x[s]);
-                load8(ur + 64 * s + 8, x[s] + 8);
-#pragma unroll
-                for (int e = 0; e < 16; ++e) m = fmaxf(m, fabsf(x[s][e]));
-            }
-            m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
-            m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
+            float u[4];
+            widen4(ur, u);
+            const float m = warp_max(fmaxf(fmaxf(fabsf(u[0]), fabsf(u[1])), fmaxf(fabsf(u[2]), fabsf(u[3]))));
             const int sh = min(7 - ((int)(__float_as_uint(m) >> 23) - 127), 120);
             const float f = exp2_int(sh);
             fu = scale * exp2_int(-sh) * sc;
+            uint32_t pa[NU], pb[NU];
+            pieces(u[0] * f, u[1] * f, pa);
+            pieces(u[2] * f, u[3] * f, pb);
+            __syncwarp();
+            if (4 * r < D / 4)
 #pragma unroll
-            for (int s = 0; s < D / 64; ++s)
+                for (int c = 0; c < NU; ++c) s_u[warp][4 * r + t][c] = pa[c] | (pb[c] << 16);
+            __syncwarp();
 #pragma unroll
-                for (int w = 0; w < 4; ++w)
-                    ub[2 * s + w / 2][w & 1] = piece_pair(x[s][4 * w] * f, x[s][4 * w + 1] * f, r) |
-                                               (piece_pair(x[s][4 * w + 2] * f, x[s][4 * w + 3] * f, r) << 16);
+            for (int w = 0; w < 2 * KS; ++w) ub[w >> 1][w & 1] = s_u[warp][4 * w + t][r];
         }
 
         // logits of rows r and r + 8 of each tile
@@ -178,6 +208,30 @@ __global__ void __launch_bounds__(32 * kWarps, kBlocksPerSm)
             y += __shfl_xor_sync(0xFFFFFFFFu, y, o);
         }
 
+        // p's pieces: the four lanes of a row hold the same values, lane t splits those of tiles t, t + 4 (rows r, r + 8).
+        // The word of lane t holds rows 2t, 2t + 1, 2t + 8, 2t + 9, as a V tile's columns do.
+#pragma unroll
+        for (int m0 = 0; m0 < MT; m0 += 4) {
+            float v0 = x[m0][0], v1 = x[m0][1];
+#pragma unroll
+            for (int q = 1; q < 4; ++q)
+                if (m0 + q < MT && t == q) {
+                    v0 = x[m0 + q][0];
+                    v1 = x[m0 + q][1];
+                }
+            uint32_t pc[NP];
+            pieces(v0 * 255.0f, v1 * 255.0f, pc);
+            if (m0 + t < MT) {
+                uint8_t *b = reinterpret_cast<uint8_t *>(&s_p[warp][m0 + t][0][r >> 1]) + (r & 1);
+#pragma unroll
+                for (int c = 0; c < NP; ++c) {
+                    b[16 * c] = (uint8_t)pc[c];
+                    b[16 * c + 2] = (uint8_t)(pc[c] >> 8);
+                }
+            }
+        }
+        __syncwarp();
+
         // sum of p k: tile (w, hw) rows r / r + 8 are d = (D / 8) r + 4 w + 2 hw (+ 1)
         float o[DT][4];
 #pragma unroll
@@ -186,24 +240,15 @@ __global__ void __launch_bounds__(32 * kWarps, kBlocksPerSm)
             for (int e = 0; e < 4; ++e) o[i][e] = 0.f;
 #pragma unroll
         for (int m = 0; m < MT; m += 2) {
-            uint32_t pb[2];
-#pragma unroll
-            for (int u = 0; u < 2; ++u) {
-                // keys 2t, 2t + 1 of the tile's first and second eight rows
-                float v[4];
-#pragma unroll
-                for (int q = 0; q < 4; ++q)
-                    v[q] = __shfl_sync(0xFFFFFFFFu, x[m + u][q >> 1], 4 * (2 * t + (q & 1))) * 255.0f;
-                pb[u] = piece_pair(v[0], v[1], r) | (piece_pair(v[2], v[3], r) << 16);
-            }
+            const uint32_t b0 = s_p[warp][m][r][t], b1 = s_p[warp][m + 1][r][t];
             const uint32_t *v0 = buf[(MT + m) & 3], *v1 = buf[(MT + m + 1) & 3];
 #pragma unroll
             for (int w = 0; w < W; ++w) {
                 uint32_t ta[4], tb[4];
                 transpose4(v0[w], v0[W + w], v0[2 * W + w], v0[3 * W + w], ta);
                 transpose4(v1[w], v1[W + w], v1[2 * W + w], v1[3 * W + w], tb);
-                mma_e4m3(o[2 * w], ta[0], ta[1], tb[0], tb[1], pb[0], pb[1]);
-                mma_e4m3(o[2 * w + 1], ta[2], ta[3], tb[2], tb[3], pb[0], pb[1]);
+                mma_e4m3(o[2 * w], ta[0], ta[1], tb[0], tb[1], b0, b1);
+                mma_e4m3(o[2 * w + 1], ta[2], ta[3], tb[2], tb[3], b0, b1);
             }
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
@@ -211,21 +256,44 @@ __global__ void __launch_bounds__(32 * kWarps, kBlocksPerSm)
                 if (n < 2 * MT) load_tile(n, a);
                 else if (more) load_tile(n - 2 * MT, an);
             }
+            if (m == 0 && more) ur = load_u(an);
         }
         const float inv = 1.0f / z, g = inv * sc * (1.0f / 255.0f);
+        if (more) sc = __ldg(ks + an.crow);
+
+        // the columns' sums: v[4 w + q] is this lane's share of d = (D / 8) r + 4 w + q; lane t keeps the sums of w = t
+        float v[4 * W];
 #pragma unroll
-        for (int w = 0; w < W; ++w) {
-            float v[4];
+        for (int i = 0; i < 4 * W; ++i) {
+            const float(&e)[4] = o[i >> 1];
+            v[i] = fmaf(e[2 * (i & 1) + 1], f1, e[2 * (i & 1)] * f0);
+        }
+        if constexpr (W == 4) {
+            float h[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {   // w = t mod 2 stay
+                const int w = (i >> 2) * 2, q = i & 3;
+                const float keep = (t & 1) ? v[4 * (w + 1) + q] : v[4 * w + q];
+                const float give = (t & 1) ? v[4 * w + q] : v[4 * (w + 1) + q];
+                h[i] = keep + __shfl_xor_sync(0xFFFFFFFFu, give, 1);
+            }
+            float k4[4];
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
-                const float(&e)[4] = o[2 * w + (q >> 1)];
-                v[q] = sum_t(fmaf(e[2 * (q & 1) + 1], f1, e[2 * (q & 1)] * f0)) * g;
+                const float keep = (t & 2) ? h[4 + q] : h[q], give = (t & 2) ? h[q] : h[4 + q];
+                k4[q] = (keep + __shfl_xor_sync(0xFFFFFFFFu, give, 2)) * g;
             }
-            if ((w & 3) == t) store4(L + crow * D + (D / 8) * r + 4 * w, v[0], v[1], v[2], v[3]);
+            store4(L + a.crow * D + (D / 8) * r + 4 * t, k4[0], k4[1], k4[2], k4[3]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4 * W; ++i) v[i] = sum_t(v[i]) * g;
+#pragma unroll
+            for (int w = 0; w < W; ++w)
+                if (t == w) store4(L + a.crow * D + (D / 8) * r + 4 * w, v[4 * w], v[4 * w + 1], v[4 * w + 2], v[4 * w + 3]);
         }
-        if (beta && lane == 0) beta[crow] = logf(z) - y * inv;
+        if (beta && lane == 0) beta[a.crow] = logf(z) - y * inv;
         if (!more) return;
-        unit = next;
+        unit += step;
         a = an;
     }
 }
