@@ -26,6 +26,8 @@
 //
 // A row's slots are split over the warps of one block or of a cluster of blocks, and the partial rows meet in shared
 // memory (distributed shared memory for a cluster): no workspace, no atomics, a fixed order.
+#include <type_traits>
+
 #include "attend_simt.cuh"
 #include "cache8.h"
 #include "sm100.cuh"
@@ -84,22 +86,24 @@ __global__ void __launch_bounds__(32 * kWarps, blocks_per_sm(D, C, sizeof(Tin) =
     // A chunk is a stream of 2 MT tiles, its keys' and then its values', through four register buffers: once tile n
     // is used, its buffer is loaded with tile n + 4 of the stream, which runs on into the warp's next chunk.
     uint32_t buf[4][WORDS];
-    auto load_tile = [&](int n, int c, int left) {   // tile n of chunk c, of which `left` keys are seen
-        if (n < MT) load_k<D>(buf[n & 3], Kb + ((size_t)c * C + 16 * n) * D, r, left - 16 * n);
-        else load_v<D>(buf[n & 3], Vb + ((size_t)c * C + 16 * (n - MT)) * D, t, left - 16 * (n - MT));
+    auto load_tile = [&](auto part, int n, int c, int top) {   // tile n of chunk c, whose last row seen is `top`
+        constexpr bool PART = decltype(part)::value;
+        if (n < MT) load_k<D, PART>(buf[n & 3], Kb + ((size_t)c * C + 16 * n) * D, r, top - 16 * n);
+        else load_v<D, PART>(buf[n & 3], Vb + ((size_t)c * C + 16 * (n - MT)) * D, t, top - 16 * (n - MT));
     };
 
-    // this warp's slots are me, me + nw, ..; the first one's tiles are asked for before anything else
+    // The own chunk, whose rows behind the query are not seen, is the first in the order of work and past chunks (whole
+    // ones) follow: turn 0 is slot k, turn x > 0 slot x - 1.  This warp's turns are me, me + nw, ..
     auto chunk_of = [&](int j) { return j < p.k ? __ldg(si + j) : j == p.k ? ci : -1; };
-    auto seen = [&](int c) { return (int)min((long long)C, pos - (long long)c * C + 1); };
-    int j = me;
-    int c = chunk_of(j);
-    while (c < 0 && j + nw < ns) { j += nw; c = chunk_of(j); }
-    int nv = 0;
-    if (c >= 0) {
-        nv = seen(c);
+    int turn = me, c = turn == 0 ? ci : chunk_of(turn <= p.k ? turn - 1 : ns);
+    while (c < 0 && turn + nw < ns) { turn += nw; c = chunk_of(turn - 1); }
+    const int own_top = (int)(pos - (long long)ci * C);
+    if (turn == 0) {
 #pragma unroll
-        for (int n = 0; n < 4; ++n) load_tile(n, c, nv);
+        for (int n = 0; n < 4; ++n) load_tile(std::true_type(), n, c, own_top);
+    } else if (c >= 0) {
+#pragma unroll
+        for (int n = 0; n < 4; ++n) load_tile(std::false_type(), n, c, C - 1);
     }
 
     // the query rows: lane (r, t) holds head h0 + r at d = 64 s + 16 t .. + 15
@@ -177,10 +181,18 @@ __global__ void __launch_bounds__(32 * kWarps, blocks_per_sm(D, C, sizeof(Tin) =
         for (int e = 0; e < 4; ++e) oacc[a][e] = 0.f;
 
     while (c >= 0) {
-        // the next slot of this warp that holds a chunk
-        int jn = j, cn = -1;
-        while (cn < 0 && jn + nw < ns) { jn += nw; cn = s_chunk[jn]; }
-        const int nvn = cn >= 0 ? seen(cn) : 0;
+        // the next turn of this warp that holds a chunk
+        int tn = turn, cn = -1;
+        while (cn < 0 && tn + nw < ns) { tn += nw; cn = s_chunk[tn - 1]; }
+        const bool own = turn == 0;
+        auto load_next = [&](int n) {
+            if (n < 2 * MT) {
+                if (own) load_tile(std::true_type(), n, c, own_top);
+                else load_tile(std::false_type(), n, c, C - 1);
+            } else if (cn >= 0) {
+                load_tile(std::false_type(), n - 2 * MT, cn, C - 1);
+            }
+        };
         const float kc = __ldg(ks + bg * p.nL + c);
         const float f0 = fq0 * kc, f1 = fq1 * kc;
 
@@ -203,48 +215,46 @@ __global__ void __launch_bounds__(32 * kWarps, blocks_per_sm(D, C, sizeof(Tin) =
                 }
             }
 #pragma unroll
-            for (int u = 0; u < 2; ++u) {
-                const int n = m + u + 4;
-                if (n < 2 * MT) load_tile(n, c, nv);
-                else if (cn >= 0) load_tile(n - 2 * MT, cn, nvn);
-            }
+            for (int u = 0; u < 2; ++u) load_next(m + u + 4);
         }
 
-        // softmax over the keys seen (rows r, r + 8 of each tile, then across the lanes of a column)
+        // softmax over the keys seen (rows r, r + 8 of each tile, then across the lanes of a column).  Rows of the own
+        // chunk that the query does not see hold its last row again: they do not change the maximum and weigh nothing.
         float m0 = -INFINITY, m1 = -INFINITY;
 #pragma unroll
-        for (int m = 0; m < MT; ++m)
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                if (16 * m + 8 * h + r < nv) {
-                    m0 = fmaxf(m0, sacc[m][2 * h] * f0);
-                    m1 = fmaxf(m1, sacc[m][2 * h + 1] * f1);
-                }
-            }
+        for (int m = 0; m < MT; ++m) {
+            m0 = fmaxf(m0, fmaxf(sacc[m][0] * f0, sacc[m][2] * f0));
+            m1 = fmaxf(m1, fmaxf(sacc[m][1] * f1, sacc[m][3] * f1));
+        }
 #pragma unroll
         for (int o = 4; o < 32; o <<= 1) {
             m0 = fmaxf(m0, __shfl_xor_sync(0xFFFFFFFFu, m0, o));
             m1 = fmaxf(m1, __shfl_xor_sync(0xFFFFFFFFu, m1, o));
         }
-        float l0 = 0.f, l1 = 0.f;
 #pragma unroll
         for (int m = 0; m < MT; ++m)
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const bool in = 16 * m + 8 * h + r < nv;
-                const float e0 = in ? exp2f(fmaf(sacc[m][2 * h], f0, -m0)) : 0.f;
-                const float e1 = in ? exp2f(fmaf(sacc[m][2 * h + 1], f1, -m1)) : 0.f;
-                sacc[m][2 * h] = e0;
-                sacc[m][2 * h + 1] = e1;
-                l0 += e0;
-                l1 += e1;
-            }
+            for (int e = 0; e < 4; ++e) sacc[m][e] = exp2f(fmaf(sacc[m][e], (e & 1) ? f1 : f0, (e & 1) ? -m1 : -m0));
+        if (own) {
+#pragma unroll
+            for (int m = 0; m < MT; ++m)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (16 * m + 8 * (e >> 1) + r > own_top) sacc[m][e] = 0.f;
+        }
+        float l0 = 0.f, l1 = 0.f;
+#pragma unroll
+        for (int m = 0; m < MT; ++m) {
+            l0 += sacc[m][0] + sacc[m][2];
+            l1 += sacc[m][1] + sacc[m][3];
+        }
 #pragma unroll
         for (int o = 4; o < 32; o <<= 1) {
             l0 += __shfl_xor_sync(0xFFFFFFFFu, l0, o);
             l1 += __shfl_xor_sync(0xFFFFFFFFu, l1, o);
         }
-        const float g0 = s_w[2 * t][j] / l0, g1 = s_w[2 * t + 1][j] / l1;
+        const int slot = own ? p.k : turn - 1;
+        const float g0 = s_w[2 * t][slot] / l0, g1 = s_w[2 * t + 1][slot] / l1;
 
         // values
 #pragma unroll
@@ -273,13 +283,10 @@ __global__ void __launch_bounds__(32 * kWarps, blocks_per_sm(D, C, sizeof(Tin) =
                     if constexpr (PHL) mma_f16(oacc[2 * w + hw], a0, a1, a2, a3, c0, c1);
                 }
             }
-            const int n = MT + m + 4;
-            if (n < 2 * MT) load_tile(n, c, nv);
-            else if (cn >= 0) load_tile(n - 2 * MT, cn, nvn);
+            load_next(MT + m + 4);
         }
-        j = jn;
+        turn = tn;
         c = cn;
-        nv = nvn;
     }
 
     // the warps' rows meet: tile a, row r is d = (D / 8) r + 2 a, row r + 8 the next one; columns are heads 2t, 2t + 1

@@ -85,7 +85,8 @@ __device__ __forceinline__ void store4(__nv_bfloat16 *p, float a, float b, float
     *reinterpret_cast<uint2 *>(p) = make_uint2(*reinterpret_cast<const uint32_t *>(&x), *reinterpret_cast<const uint32_t *>(&y));
 }
 
-template <typename Tin, int D, int C>
+// PART: the one chunk that t_end ends inside; otherwise whole chunks.
+template <typename Tin, int D, int C, bool PART>
 __global__ void __launch_bounds__(32 * kWarps, kBlocksPerSm)
     landmarks8_kernel(const uint8_t *__restrict__ K8, const float *__restrict__ ks, const Tin *__restrict__ U,
                       Tin *__restrict__ L, float *__restrict__ beta, Cache8 p, float scale, int c0, int span, int t_end)
@@ -116,14 +117,14 @@ __global__ void __launch_bounds__(32 * kWarps, kBlocksPerSm)
         const unsigned bg = u / (unsigned)span;
         const int c = c0 + (int)(u - bg * (unsigned)span);
         a.crow = (size_t)bg * p.nL + c;
-        a.rows = (int)min((long long)C, (long long)t_end - (long long)c * C);
+        a.rows = PART ? t_end - c * C : C;
         a.row0 = K8 + ((size_t)bg * p.T + (size_t)c * C) * D;
         return a;
     };
     uint32_t buf[4][WORDS];
     auto load_tile = [&](int n, const At &a) {
-        if (n < MT) load_k<D>(buf[n & 3], a.row0 + 16 * n * D + 16 * t, r, a.rows - 16 * n);
-        else load_v<D>(buf[n & 3], a.row0 + 16 * (n - MT) * D + (D / 8) * r, t, a.rows - 16 * (n - MT));
+        if (n < MT) load_k<D, PART>(buf[n & 3], a.row0 + 16 * n * D + 16 * t, r, a.rows - 1 - 16 * n);
+        else load_v<D, PART>(buf[n & 3], a.row0 + 16 * (n - MT) * D + (D / 8) * r, t, a.rows - 1 - 16 * (n - MT));
     };
     // the landmark query: lane (r, t) takes its word r of column block t (d = 64 (r / 4) + 16 t + 4 (r % 4))
     const int ud = (64 * (r >> 2) + 16 * t + 4 * (r & 3)) % D;   // d = 64: lanes of r >= 4 repeat the others
@@ -136,8 +137,7 @@ __global__ void __launch_bounds__(32 * kWarps, kBlocksPerSm)
     float sc = __ldg(ks + a.crow);
     for (;;) {
         const bool more = units - unit > step;
-        At an = a;
-        if (more) an = at(unit + step);
+        const At an = at(more ? unit + step : unit);   // behind the last chunk its own tiles again: no branch around a load
 
         // the landmark query's pieces: lane (r, t) holds piece r at d = 64 s + 16 t .. + 15
         uint32_t ub[KS][2];
@@ -177,7 +177,7 @@ __global__ void __launch_bounds__(32 * kWarps, kBlocksPerSm)
             for (int u = 0; u < 2; ++u) {
                 const int n = m + u + 4;
                 if (n < 2 * MT) load_tile(n, a);
-                else if (more) load_tile(n - 2 * MT, an);
+                else load_tile(n - 2 * MT, an);
                 x[m + u][0] = sum_t(fmaf(d[u][1], f1, d[u][0] * f0)) * fu;
                 x[m + u][1] = sum_t(fmaf(d[u][3], f1, d[u][2] * f0)) * fu;
             }
@@ -189,7 +189,7 @@ __global__ void __launch_bounds__(32 * kWarps, kBlocksPerSm)
         for (int m = 0; m < MT; ++m)
 #pragma unroll
             for (int h = 0; h < 2; ++h)
-                if (16 * m + 8 * h + r < a.rows) mx = fmaxf(mx, x[m][h]);
+                if (!PART || 16 * m + 8 * h + r < a.rows) mx = fmaxf(mx, x[m][h]);
 #pragma unroll
         for (int o = 4; o < 32; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, o));
 #pragma unroll
@@ -197,7 +197,7 @@ __global__ void __launch_bounds__(32 * kWarps, kBlocksPerSm)
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 const float d = x[m][h] - mx;
-                const float w = 16 * m + 8 * h + r < a.rows ? expf(d) : 0.f;
+                const float w = !PART || 16 * m + 8 * h + r < a.rows ? expf(d) : 0.f;
                 z += w;
                 y += w == 0.f ? 0.f : w * d;
                 x[m][h] = w;
@@ -254,12 +254,12 @@ __global__ void __launch_bounds__(32 * kWarps, kBlocksPerSm)
             for (int u = 0; u < 2; ++u) {
                 const int n = MT + m + u + 4;
                 if (n < 2 * MT) load_tile(n, a);
-                else if (more) load_tile(n - 2 * MT, an);
+                else load_tile(n - 2 * MT, an);
             }
-            if (m == 0 && more) ur = load_u(an);
+            if (m == 0) ur = load_u(an);
         }
         const float inv = 1.0f / z, g = inv * sc * (1.0f / 255.0f);
-        if (more) sc = __ldg(ks + an.crow);
+        sc = __ldg(ks + an.crow);
 
         // the columns' sums: v[4 w + q] is this lane's share of d = (D / 8) r + 4 w + q; lane t keeps the sums of w = t
         float v[4 * W];
@@ -302,11 +302,18 @@ template <typename Tin, int D, int C>
 cudaError_t launch_t(const Cache8 &c, float scale, const uint8_t *K8, const float *ks, const void *U, void *L, float *beta,
                      int c0, int c1, int t_end, cudaStream_t s)
 {
-    const long long units = (long long)c.B * c.Hkv * (c1 - c0), blocks = (units + kWarps - 1) / kWarps;
-    const unsigned grid = (unsigned)(blocks < 148 * kBlocksPerSm ? blocks : 148 * kBlocksPerSm);
-    landmarks8_kernel<Tin, D, C><<<grid, 32 * kWarps, 0, s>>>(K8, ks, static_cast<const Tin *>(U), static_cast<Tin *>(L), beta,
-                                                              c, scale, c0, c1 - c0, t_end);
-    return cudaGetLastError();
+    auto run = [&](auto kern, int first, int span) {
+        const long long units = (long long)c.B * c.Hkv * span, blocks = (units + kWarps - 1) / kWarps;
+        const unsigned grid = (unsigned)(blocks < 148 * kBlocksPerSm ? blocks : 148 * kBlocksPerSm);
+        kern<<<grid, 32 * kWarps, 0, s>>>(K8, ks, static_cast<const Tin *>(U), static_cast<Tin *>(L), beta, c, scale, first,
+                                          span, t_end);
+        return cudaGetLastError();
+    };
+    const int whole = t_end / C;   // chunks before the one that t_end ends inside
+    cudaError_t e = cudaSuccess;
+    if (c0 < whole) e = run(landmarks8_kernel<Tin, D, C, false>, c0, (c1 < whole ? c1 : whole) - c0);
+    if (e == cudaSuccess && c1 > whole) e = run(landmarks8_kernel<Tin, D, C, true>, whole, 1);
+    return e;
 }
 
 template <typename Tin, int D>

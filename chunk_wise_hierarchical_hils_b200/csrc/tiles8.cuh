@@ -28,42 +28,28 @@ __device__ __forceinline__ void ldg8(uint32_t *w, const uint8_t *p)
 }
 
 // One tile, D / 8 words a lane.  Keys: [2 rows][D / 64 segments][4 words]; values: [4 rows][D / 32 words].
-// p: the tile's first row + this lane's column (16 t, or (D / 8) r); left: the rows of the tile that may be read (16 or
-// more: all of them; the same for the whole warp).  The others become zeros.
-template <int D>
-__device__ __forceinline__ void load_k(uint32_t *w, const uint8_t *p, int r, int left)
+// p: the tile's first row + this lane's column (16 t, or (D / 8) r).  PART: rows behind row `top` (counted from the
+// tile's first; below 0 where the tile holds none) may not be read, and row `top` stands in for them.
+template <int D, bool PART = false>
+__device__ __forceinline__ void load_k(uint32_t *w, const uint8_t *p, int r, int top = 0)
 {
-    if (left >= 16) {
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-#pragma unroll
-            for (int s = 0; s < D / 64; ++s) ldg16(w + (h * (D / 64) + s) * 4, p + (8 * h + r) * D + 64 * s);
-        return;
-    }
 #pragma unroll
     for (int h = 0; h < 2; ++h)
 #pragma unroll
-        for (int s = 0; s < D / 64; ++s) {
-            uint32_t *x = w + (h * (D / 64) + s) * 4;
-            if (8 * h + r < left) ldg16(x, p + (8 * h + r) * D + 64 * s);
-            else x[0] = x[1] = x[2] = x[3] = 0u;
-        }
+        for (int s = 0; s < D / 64; ++s)
+            ldg16(w + (h * (D / 64) + s) * 4, p + (PART ? min(8 * h + r, top) : 8 * h + r) * D + 64 * s);
 }
 
-template <int D>
-__device__ __forceinline__ void load_v(uint32_t *w, const uint8_t *p, int t, int left)
+template <int D, bool PART = false>
+__device__ __forceinline__ void load_v(uint32_t *w, const uint8_t *p, int t, int top = 0)
 {
     constexpr int W = D / 32;
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
         const int key = 2 * t + (q & 1) + 8 * (q >> 1);
-        if (left >= 16 || key < left) {
-            if constexpr (W == 4) ldg16(w + q * W, p + key * D);
-            else ldg8(w + q * W, p + key * D);
-        } else {
-#pragma unroll
-            for (int x = 0; x < W; ++x) w[q * W + x] = 0u;
-        }
+        const uint8_t *src = p + (PART ? min(key, top) : key) * D;
+        if constexpr (W == 4) ldg16(w + q * W, src);
+        else ldg8(w + q * W, src);
     }
 }
 
