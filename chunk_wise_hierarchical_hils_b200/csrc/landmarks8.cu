@@ -6,16 +6,15 @@
 // bias.
 //
 // Every key byte is read once from HBM and used in two products, so the kernel is bound by HBM as long as the
-// products stay cheap: both run on e4m3 mma.sync tiles, in which the keys are operands as they are.  One warp per
-// chunk, with the pipeline of the attention kernel: a chunk is a stream of tiles, as keys (for the logits) and again as
-// values (for the sum; these loads hit L1), through four register buffers, running on into the warp's next chunk.
+// products stay cheap: one warp per chunk, mma.sync tiles of f16 (e4m3 is exact in it), with the pipeline of the
+// attention kernel: a chunk is a stream of tiles, as keys (for the logits) and again as values (for the sum; these
+// loads hit L1), through four register buffers, running on into the warp's next chunk.  (mma.sync has an e4m3 form, but
+// on this GPU it runs as conversions and two f16 products: 1134 instructions a chunk against 828 in this form.)
 //
-// Numbers.  The other operand, one row of u or p, is float32: it is split into pieces of e4m3's four bits, each 2^4 finer
-// than the one before, in the columns the product has anyway (column c holds piece c).  For float32 results six pieces
-// hold 24 bits (u relative to the row's largest, p to the chunk's largest); for bf16 ones two pieces hold a bf16 u
-// and three the 11 bits of p (2^-12 of its value, where the result's own rounding is 2^-9).  The columns' sums meet in
-// float32.  A lane splits the values it holds and the pieces change places in shared memory: splitting the row in
-// every lane that needs one piece of it took three times the instructions (2129 a chunk against 750).
+// Numbers.  The other operand, one row of u or p, is float32, scaled by a power of two to just below 2^15 (u by its
+// largest, p has 1): its f16 value is column 0 of the product and, for float32 results, what that leaves is column
+// 1 (22 bits together).  bf16 landmark queries are exact in column 0, and p's 2^-12 there is below the bf16 result's own
+// rounding (2^-9).  Sums are float32.
 #include "cache8.h"
 #include "common.cuh"
 #include "tiles8.cuh"
@@ -27,28 +26,6 @@ using namespace t8;
 
 constexpr int kWarps = 4;
 constexpr int kBlocksPerSm = 3;
-
-// The pieces of two values below 256 in magnitude: o[c] holds the e4m3 bytes of 16^c times what pieces 0 .. c - 1 leave.
-template <int N>
-__device__ __forceinline__ void pieces(float a, float b, uint32_t (&o)[N])
-{
-    static_assert(N == 2 || N == 3 || N == 6, "pieces of one or two f16 values");
-    uint32_t h = pack_f16(a, b);
-    const float2 y = unpack_f16(h);
-#pragma unroll
-    for (int c = 0; c < (N < 3 ? N : 3); ++c) {
-        o[c] = f16x2_to_e4m3x2(h);
-        h = e4m3_rest<16>(h, o[c]);
-    }
-    if constexpr (N == 6) {
-        h = pack_f16((a - y.x) * 4096.0f, (b - y.y) * 4096.0f);
-#pragma unroll
-        for (int c = 3; c < 6; ++c) {
-            o[c] = f16x2_to_e4m3x2(h);
-            h = e4m3_rest<16>(h, o[c]);
-        }
-    }
-}
 
 // Four consecutive elements, raw until they are used.
 __device__ __forceinline__ void widen4(float4 v, float *o) { o[0] = v.x; o[1] = v.y; o[2] = v.z; o[3] = v.w; }
@@ -62,27 +39,34 @@ struct Raw4 { typedef uint2 type; };
 template <>
 struct Raw4<float> { typedef float4 type; };
 
-__device__ __forceinline__ float sum_t(float x)   // over the four lanes of a row
+// What f16 leaves of two values.
+__device__ __forceinline__ uint32_t rest_f16(float a, float b, uint32_t h)
 {
-    x += __shfl_xor_sync(0xFFFFFFFFu, x, 1);
-    return x + __shfl_xor_sync(0xFFFFFFFFu, x, 2);
+    const float2 y = unpack_f16(h);
+    return pack_f16(a - y.x, b - y.y);
 }
 
-template <typename T>
-__device__ __forceinline__ void store4(T *p, float a, float b, float c, float d)
+// N consecutive results (N = 8 or 16).
+template <int N>
+__device__ __forceinline__ void store_n(float *p, const float *v)
 {
-    store_out(p, a); store_out(p + 1, b); store_out(p + 2, c); store_out(p + 3, d);
+#pragma unroll
+    for (int i = 0; i < N; i += 4) *reinterpret_cast<float4 *>(p + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
 }
-template <>
-__device__ __forceinline__ void store4(float *p, float a, float b, float c, float d)
+template <int N>
+__device__ __forceinline__ void store_n(__nv_bfloat16 *p, const float *v)
 {
-    *reinterpret_cast<float4 *>(p) = make_float4(a, b, c, d);
-}
-template <>
-__device__ __forceinline__ void store4(__nv_bfloat16 *p, float a, float b, float c, float d)
-{
-    const __nv_bfloat162 x = __floats2bfloat162_rn(a, b), y = __floats2bfloat162_rn(c, d);
-    *reinterpret_cast<uint2 *>(p) = make_uint2(*reinterpret_cast<const uint32_t *>(&x), *reinterpret_cast<const uint32_t *>(&y));
+#pragma unroll
+    for (int i = 0; i < N; i += 8) {
+        uint4 u;
+        uint32_t *w = reinterpret_cast<uint32_t *>(&u);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const __nv_bfloat162 x = __floats2bfloat162_rn(v[i + 2 * j], v[i + 2 * j + 1]);
+            w[j] = *reinterpret_cast<const uint32_t *>(&x);
+        }
+        *reinterpret_cast<uint4 *>(p + i) = u;
+    }
 }
 
 // PART: the one chunk that t_end ends inside; otherwise whole chunks.
@@ -91,21 +75,20 @@ __global__ void __launch_bounds__(32 * kWarps, kBlocksPerSm)
     landmarks8_kernel(const uint8_t *__restrict__ K8, const float *__restrict__ ks, const Tin *__restrict__ U,
                       Tin *__restrict__ L, float *__restrict__ beta, Cache8 p, float scale, int c0, int span, int t_end)
 {
-    constexpr int MT = C / 16, KS = D / 32, DT = D / 16, WORDS = D / 8, W = D / 32;
+    constexpr int MT = C / 16, KS = D / 16, DT = D / 16, WORDS = D / 8, W = D / 32;
     constexpr bool F32 = sizeof(Tin) == 4;
-    constexpr int NU = F32 ? 6 : 2, NP = F32 ? 6 : 3;   // pieces of u and of p
+    constexpr float PTOP = 32768.0f;
     typedef typename Raw4<Tin>::type Raw;
-    // pieces on their way between lanes: u's as [word of the row][piece] (a word: four values), p's as [tile][piece][lane t]
-    __shared__ __align__(16) uint32_t s_u[kWarps][D / 4][8];
-    __shared__ uint32_t s_p[kWarps][MT][8][4];
+    // the landmark query's columns 0, 1 (and 2: zeros, for all the others): [column][t][word: two values]
+    __shared__ __align__(16) uint32_t s_u[kWarps][3][4][2 * KS + 4];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = lane >> 2, t = lane & 3;
     const unsigned units = (unsigned)(p.B * p.Hkv) * (unsigned)span, step = gridDim.x * kWarps;
-    const float f0 = exp2_int(-8 * t), f1 = exp2_int(-8 * t - 4);   // worth of pieces 2t and 2t + 1
 
     unsigned unit = blockIdx.x * kWarps + warp;
     if (unit >= units) return;   // whole warps leave; no block barrier follows
-    for (int i = lane; i < D / 4 * 8; i += 32) (&s_u[warp][0][0])[i] = 0u;   // columns without a piece stay zero
-    for (int i = lane; i < MT * 32; i += 32) (&s_p[warp][0][0][0])[i] = 0u;
+    if (r < 2 * KS / 4)   // columns without a value stay zero
+#pragma unroll
+        for (int c = 1; c < 3; ++c) *reinterpret_cast<uint4 *>(&s_u[warp][c][t][4 * r]) = make_uint4(0u, 0u, 0u, 0u);
 
     struct At {
         size_t crow;
@@ -139,29 +122,33 @@ __global__ void __launch_bounds__(32 * kWarps, kBlocksPerSm)
         const bool more = units - unit > step;
         const At an = at(more ? unit + step : unit);   // behind the last chunk its own tiles again: no branch around a load
 
-        // the landmark query's pieces: lane (r, t) holds piece r at d = 64 s + 16 t .. + 15
+        // the landmark query: lane (r, t) holds column r at d = 64 s + 16 t .. + 15
         uint32_t ub[KS][2];
         float fu;
         {
             float u[4];
             widen4(ur, u);
             const float m = warp_max(fmaxf(fmaxf(fabsf(u[0]), fabsf(u[1])), fmaxf(fabsf(u[2]), fabsf(u[3]))));
-            const int sh = min(7 - ((int)(__float_as_uint(m) >> 23) - 127), 120);
+            const int sh = min(14 - ((int)(__float_as_uint(m) >> 23) - 127), 120);
             const float f = exp2_int(sh);
             fu = scale * exp2_int(-sh) * sc;
-            uint32_t pa[NU], pb[NU];
-            pieces(u[0] * f, u[1] * f, pa);
-            pieces(u[2] * f, u[3] * f, pb);
+            const uint32_t h0 = pack_f16(u[0] * f, u[1] * f), h1 = pack_f16(u[2] * f, u[3] * f);
             __syncwarp();
-            if (4 * r < D / 4)
-#pragma unroll
-                for (int c = 0; c < NU; ++c) s_u[warp][4 * r + t][c] = pa[c] | (pb[c] << 16);
+            if (r < KS) {
+                *reinterpret_cast<uint2 *>(&s_u[warp][0][t][2 * r]) = make_uint2(h0, h1);
+                if constexpr (F32)
+                    *reinterpret_cast<uint2 *>(&s_u[warp][1][t][2 * r]) =
+                        make_uint2(rest_f16(u[0] * f, u[1] * f, h0), rest_f16(u[2] * f, u[3] * f, h1));
+            }
             __syncwarp();
 #pragma unroll
-            for (int w = 0; w < 2 * KS; ++w) ub[w >> 1][w & 1] = s_u[warp][4 * w + t][r];
+            for (int k = 0; k < KS; k += 2) {
+                const uint4 v = *reinterpret_cast<const uint4 *>(&s_u[warp][min(r, 2)][t][2 * k]);
+                ub[k][0] = v.x; ub[k][1] = v.y; ub[k + 1][0] = v.z; ub[k + 1][1] = v.w;
+            }
         }
 
-        // logits of rows r and r + 8 of each tile
+        // logits of rows r and r + 8 of each tile: columns 0 and 1 are lane t = 0's (the others' are zeros and stay unused)
         float x[MT][2];
 #pragma unroll
         for (int m = 0; m < MT; m += 2) {
@@ -170,16 +157,17 @@ __global__ void __launch_bounds__(32 * kWarps, kBlocksPerSm)
             for (int kk = 0; kk < KS; ++kk)
 #pragma unroll
                 for (int u = 0; u < 2; ++u) {
-                    const uint32_t *w = buf[(m + u) & 3];
-                    mma_e4m3(d[u], w[2 * kk], w[2 * KS + 2 * kk], w[2 * kk + 1], w[2 * KS + 2 * kk + 1], ub[kk][0], ub[kk][1]);
+                    const uint32_t w0 = buf[(m + u) & 3][kk], w1 = buf[(m + u) & 3][KS + kk];
+                    mma_f16(d[u], e4m3x2_to_f16x2(w0), e4m3x2_to_f16x2(w1), e4m3x2_to_f16x2(w0 >> 16),
+                            e4m3x2_to_f16x2(w1 >> 16), ub[kk][0], ub[kk][1]);
                 }
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
                 const int n = m + u + 4;
                 if (n < 2 * MT) load_tile(n, a);
                 else load_tile(n - 2 * MT, an);
-                x[m + u][0] = sum_t(fmaf(d[u][1], f1, d[u][0] * f0)) * fu;
-                x[m + u][1] = sum_t(fmaf(d[u][3], f1, d[u][2] * f0)) * fu;
+                x[m + u][0] = (d[u][0] + d[u][1]) * fu;
+                x[m + u][1] = (d[u][2] + d[u][3]) * fu;
             }
         }
 
@@ -208,30 +196,6 @@ __global__ void __launch_bounds__(32 * kWarps, kBlocksPerSm)
             y += __shfl_xor_sync(0xFFFFFFFFu, y, o);
         }
 
-        // p's pieces: the four lanes of a row hold the same values, lane t splits those of tiles t, t + 4 (rows r, r + 8).
-        // The word of lane t holds rows 2t, 2t + 1, 2t + 8, 2t + 9, as a V tile's columns do.
-#pragma unroll
-        for (int m0 = 0; m0 < MT; m0 += 4) {
-            float v0 = x[m0][0], v1 = x[m0][1];
-#pragma unroll
-            for (int q = 1; q < 4; ++q)
-                if (m0 + q < MT && t == q) {
-                    v0 = x[m0 + q][0];
-                    v1 = x[m0 + q][1];
-                }
-            uint32_t pc[NP];
-            pieces(v0 * 255.0f, v1 * 255.0f, pc);
-            if (m0 + t < MT) {
-                uint8_t *b = reinterpret_cast<uint8_t *>(&s_p[warp][m0 + t][0][r >> 1]) + (r & 1);
-#pragma unroll
-                for (int c = 0; c < NP; ++c) {
-                    b[16 * c] = (uint8_t)pc[c];
-                    b[16 * c + 2] = (uint8_t)(pc[c] >> 8);
-                }
-            }
-        }
-        __syncwarp();
-
         // sum of p k: tile (w, hw) rows r / r + 8 are d = (D / 8) r + 4 w + 2 hw (+ 1)
         float o[DT][4];
 #pragma unroll
@@ -239,57 +203,43 @@ __global__ void __launch_bounds__(32 * kWarps, kBlocksPerSm)
 #pragma unroll
             for (int e = 0; e < 4; ++e) o[i][e] = 0.f;
 #pragma unroll
-        for (int m = 0; m < MT; m += 2) {
-            const uint32_t b0 = s_p[warp][m][r][t], b1 = s_p[warp][m + 1][r][t];
-            const uint32_t *v0 = buf[(MT + m) & 3], *v1 = buf[(MT + m + 1) & 3];
+        for (int m = 0; m < MT; ++m) {
+            // column r of p for keys 2t, 2t + 1 and 2t + 8, 2t + 9 of the tile
+            uint32_t b[2];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const float v0 = __shfl_sync(0xFFFFFFFFu, x[m][h], 8 * t) * PTOP;
+                const float v1 = __shfl_sync(0xFFFFFFFFu, x[m][h], 8 * t + 4) * PTOP;
+                const uint32_t hi = pack_f16(v0, v1);
+                b[h] = r == 0 ? hi : 0u;
+                if constexpr (F32) b[h] = r == 1 ? rest_f16(v0, v1, hi) : b[h];
+            }
+            const uint32_t *v = buf[(MT + m) & 3];
 #pragma unroll
             for (int w = 0; w < W; ++w) {
-                uint32_t ta[4], tb[4];
-                transpose4(v0[w], v0[W + w], v0[2 * W + w], v0[3 * W + w], ta);
-                transpose4(v1[w], v1[W + w], v1[2 * W + w], v1[3 * W + w], tb);
-                mma_e4m3(o[2 * w], ta[0], ta[1], tb[0], tb[1], b0, b1);
-                mma_e4m3(o[2 * w + 1], ta[2], ta[3], tb[2], tb[3], b0, b1);
-            }
 #pragma unroll
-            for (int u = 0; u < 2; ++u) {
-                const int n = MT + m + u + 4;
-                if (n < 2 * MT) load_tile(n, a);
-                else load_tile(n - 2 * MT, an);
+                for (int hw = 0; hw < 2; ++hw) {
+                    const uint32_t lo = __byte_perm(v[w], v[W + w], hw ? 0x7362 : 0x5140);
+                    const uint32_t hi = __byte_perm(v[2 * W + w], v[3 * W + w], hw ? 0x7362 : 0x5140);
+                    mma_f16(o[2 * w + hw], e4m3x2_to_f16x2(lo), e4m3x2_to_f16x2(lo >> 16), e4m3x2_to_f16x2(hi),
+                            e4m3x2_to_f16x2(hi >> 16), b[0], b[1]);
+                }
             }
+            const int n = MT + m + 4;
+            if (n < 2 * MT) load_tile(n, a);
+            else load_tile(n - 2 * MT, an);
             if (m == 0) ur = load_u(an);
         }
-        const float inv = 1.0f / z, g = inv * sc * (1.0f / 255.0f);
+        const float inv = 1.0f / z, g = inv * sc * (1.0f / PTOP);
         sc = __ldg(ks + an.crow);
-
-        // the columns' sums: v[4 w + q] is this lane's share of d = (D / 8) r + 4 w + q; lane t keeps the sums of w = t
-        float v[4 * W];
+        if (t == 0) {
+            float v[2 * DT];
 #pragma unroll
-        for (int i = 0; i < 4 * W; ++i) {
-            const float(&e)[4] = o[i >> 1];
-            v[i] = fmaf(e[2 * (i & 1) + 1], f1, e[2 * (i & 1)] * f0);
-        }
-        if constexpr (W == 4) {
-            float h[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {   // w = t mod 2 stay
-                const int w = (i >> 2) * 2, q = i & 3;
-                const float keep = (t & 1) ? v[4 * (w + 1) + q] : v[4 * w + q];
-                const float give = (t & 1) ? v[4 * w + q] : v[4 * (w + 1) + q];
-                h[i] = keep + __shfl_xor_sync(0xFFFFFFFFu, give, 1);
+            for (int i = 0; i < DT; ++i) {
+                v[2 * i] = (o[i][0] + o[i][1]) * g;
+                v[2 * i + 1] = (o[i][2] + o[i][3]) * g;
             }
-            float k4[4];
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                const float keep = (t & 2) ? h[4 + q] : h[q], give = (t & 2) ? h[q] : h[4 + q];
-                k4[q] = (keep + __shfl_xor_sync(0xFFFFFFFFu, give, 2)) * g;
-            }
-            store4(L + a.crow * D + (D / 8) * r + 4 * t, k4[0], k4[1], k4[2], k4[3]);
-        } else {
-#pragma unroll
-            for (int i = 0; i < 4 * W; ++i) v[i] = sum_t(v[i]) * g;
-#pragma unroll
-            for (int w = 0; w < W; ++w)
-                if (t == w) store4(L + a.crow * D + (D / 8) * r + 4 * w, v[4 * w], v[4 * w + 1], v[4 * w + 2], v[4 * w + 3]);
+            store_n<2 * DT>(L + a.crow * D + (D / 8) * r, v);
         }
         if (beta && lane == 0) beta[a.crow] = logf(z) - y * inv;
         if (!more) return;

@@ -62,33 +62,12 @@ __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1,
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// D (16 x 8, f32) += A (16 x 32, e4m3) B (32 x 8): a quarter of the f16 product's cycles per element on B200 (4.6 against
-// 2 x 8 a warp), with float32 sums (errors of 2^-24 of the largest term measured)
-__device__ __forceinline__ void mma_e4m3(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
-                                         uint32_t b1)
-{
-    asm("mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
-        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-
 // 8 x 8 matrix of 16-bit elements, transposed across the warp
 __device__ __forceinline__ uint32_t movmatrix_t(uint32_t x)
 {
     uint32_t y;
     asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
     return y;
-}
-
-// Four rows of four bytes -> four columns: o[x] = byte x of a, b, c, d.
-__device__ __forceinline__ void transpose4(uint32_t a, uint32_t b, uint32_t c, uint32_t d, uint32_t (&o)[4])
-{
-    const uint32_t ab0 = __byte_perm(a, b, 0x5140), ab1 = __byte_perm(a, b, 0x7362);   // a0 b0 a1 b1, a2 b2 a3 b3
-    const uint32_t cd0 = __byte_perm(c, d, 0x5140), cd1 = __byte_perm(c, d, 0x7362);
-    o[0] = __byte_perm(ab0, cd0, 0x5410);
-    o[1] = __byte_perm(ab0, cd0, 0x7632);
-    o[2] = __byte_perm(ab1, cd1, 0x5410);
-    o[3] = __byte_perm(ab1, cd1, 0x7632);
 }
 
 __device__ __forceinline__ uint32_t pack_f16(float lo, float hi)
@@ -98,25 +77,6 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi)
 }
 
 __device__ __forceinline__ float2 unpack_f16(uint32_t v) { return __half22float2(*reinterpret_cast<const __half2 *>(&v)); }
-
-// Two f16 values -> two e4m3 bytes (low 16 bits), nearest even.
-__device__ __forceinline__ uint32_t f16x2_to_e4m3x2(uint32_t h)
-{
-    uint16_t r;
-    asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(r) : "r"(h));
-    return r;
-}
-
-// What two e4m3 bytes leave of the two f16 values they round, times SCALE (16 or 1): exact in f16, the difference having
-// at most the value's bits below the top four.
-template <int SCALE>
-__device__ __forceinline__ uint32_t e4m3_rest(uint32_t h, uint32_t bytes)
-{
-    const uint32_t b = e4m3x2_to_f16x2(bytes);
-    __half2 d = __hsub2(*reinterpret_cast<const __half2 *>(&h), *reinterpret_cast<const __half2 *>(&b));
-    if constexpr (SCALE != 1) d = __hmul2(d, __float2half2_rn((float)SCALE));
-    return *reinterpret_cast<const uint32_t *>(&d);
-}
 
 }  // namespace t8
 }  // namespace hils
