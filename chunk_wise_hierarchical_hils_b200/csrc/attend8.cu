@@ -26,6 +26,8 @@
 //
 // A row's slots are split over the warps of one block or of a cluster of blocks, and the partial rows meet in shared
 // memory (distributed shared memory for a cluster): no workspace, no atomics, a fixed order.
+#include <stdlib.h>
+#include <string.h>
 #include <type_traits>
 
 #include "attend_simt.cuh"
@@ -372,10 +374,21 @@ cudaError_t launch_d(const Dims &p, const void *Q, const uint8_t *K8, const uint
 
 size_t attend8_ws_bytes(const Dims &, hils_dtype, hils_dtype) { return 0; }
 
+// Test control: HILS_Q8_KERNEL=rows or =union forces the kernel (the latter where it covers the shape).
+static bool use_union(const Dims &p, hils_dtype in, hils_dtype out)
+{
+    if (!attend8_tc_supported(p, in, out)) return false;
+    const char *force = getenv("HILS_Q8_KERNEL");
+    if (force && strcmp(force, "rows") == 0) return false;
+    if (force && strcmp(force, "union") == 0) return true;
+    return p.N >= 64;
+}
+
 cudaError_t launch_attend8(const Dims &p, hils_dtype in, hils_dtype out, const void *Q, const uint8_t *K8,
                            const uint8_t *V8, const float *ks, const float *vs, const int32_t *sel_idx,
-                           const float *sel_score, void *O, void *, const DeviceCtl &, cudaStream_t s)
+                           const float *sel_score, void *O, void *, const DeviceCtl &ctl, cudaStream_t s)
 {
+    if (use_union(p, in, out)) return launch_attend8_tc(p, Q, K8, V8, ks, vs, sel_idx, sel_score, O, ctl, s);
     if (in == HILS_F32)
         return out == HILS_F32 ? launch_d<float, float>(p, Q, K8, V8, ks, vs, sel_idx, sel_score, O, s)
                                : launch_d<float, __nv_bfloat16>(p, Q, K8, V8, ks, vs, sel_idx, sel_score, O, s);

@@ -20,6 +20,12 @@ cudaError_t launch_cache_read(const Cache8 &c, hils_dtype out, const uint8_t *K8
 cudaError_t launch_landmarks8(const Cache8 &c, hils_dtype in, float scale, const uint8_t *K8, const float *ks,
                               const void *U, void *L, float *beta, int c0, int c1, int t_end, cudaStream_t s);
 
+// Chunk attention over the 8-bit cache: rows of work (every shape and type), or the union of a query block's chunks on
+// the tensor cores (bf16 in and out, d = 128, C = 64).
+bool attend8_tc_supported(const Dims &p, hils_dtype in, hils_dtype out);
+cudaError_t launch_attend8_tc(const Dims &p, const void *Q, const uint8_t *K8, const uint8_t *V8, const float *ks,
+                              const float *vs, const int32_t *sel_idx, const float *sel_score, void *O,
+                              const DeviceCtl &ctl, cudaStream_t s);
 size_t attend8_ws_bytes(const Dims &p, hils_dtype in, hils_dtype out);
 cudaError_t launch_attend8(const Dims &p, hils_dtype in, hils_dtype out, const void *Q, const uint8_t *K8,
                            const uint8_t *V8, const float *ks, const float *vs, const int32_t *sel_idx,
