@@ -11,21 +11,25 @@
 //               and is the sum of two e4m3 values (8 bits in two times 4; elements below 2^-10 of the row's largest lose
 //               up to 2^-18 of it), so two products replace a conversion of every key tile.
 //   O += P V    kind::f16: the probabilities keep f16's 11 bits (three e4m3 products would be needed for
-//               that), so a value tile is widened to f16 (exact) in shared memory by the warps that make its
-//               probabilities, while its scores are being multiplied.
+//               that), so value tiles are widened to f16 (exact) in shared memory by four warps of their own.
+//               (By the softmax warps, between their other work, the 8K prefill took 946 us.)
 // What a row's weights w_c vs_c are divided by is the row's own largest, times 2^-14: f16 holds 2^-12 of a
 // weight down to 2^-28 of the largest, and the row is multiplied back in float32 at the end.
 //
 // Roles, meeting on mbarriers (pair p = chunks 2p, 2p + 1 of the union; buffers go by p % 2):
 //   warp 0  TMA of key pairs    (K_LAND; a slot frees with the key product, QK_DONE)
-//   warp 1  TMA of value pairs  (V8_LAND; a slot frees when eight warps have widened it, V8_FREE); TMEM
+//   warp 1  TMA of value pairs  (V8_LAND; a slot frees when four warps have widened it, V8_FREE); TMEM
 //   warp 2  key products        (after K_LAND and S_FREE, the eight warps' reads of pair p - 2; announces QK_DONE)
-//   warp 3  value products      (after PV_READY, eight warps; announces PV_DONE)
-//   warps 4..15  three groups of four, group t % 3 takes chunk t, a thread a row: waits for PV_DONE of pair p - 2 (frees
-//           the f16 value slot and the P buffer) and V8_LAND, widens the value tile, reads S from TMEM, writes P to it.
-// A parity wait must not run two phases ahead: a softmax warp skips pairs, but it has seen PV_DONE of pair p - 2 before it
-// waits for V8_LAND of pair p, and products complete in order.  Every wait is bounded; on expiry the CTA records
-// HILS_ERR_TIMEOUT, drains its copies and products, frees its TMEM and exits.
+//   warp 3  value products      (after PV_READY, eight warps, and V16_READY, four; announces PV_DONE)
+//   warps 4..7   widen value pairs (after V8_LAND, and PV_DONE of pair p - 2, which frees the f16 slot)
+//   warps 8..19  three softmax groups of four, group t % 3 takes chunk t, a thread a row: reads S from TMEM, writes P to it
+//           (after PV_DONE of pair p - 2)
+// A parity wait must not run two phases ahead: a softmax warp skips pairs, but one that waits for PV_DONE of pair p - 2 has
+// seen that of p - 4 or of a later pair, and products complete in order.  Every wait is bounded; on expiry the CTA
+// records HILS_ERR_TIMEOUT, drains its copies and products, frees its TMEM and exits.
+//
+// Registers: 640 threads start with 96 each; the first four warps keep 40, the widening ones 56 and the softmax
+// warps take 128 (the sum of the shares is what the block was launched with, which the host checks).
 #include <cuda.h>
 #include <cuda_fp16.h>
 
@@ -41,7 +45,11 @@ namespace {
 using namespace sm100;
 
 constexpr int kGroups = 3;
-constexpr int kThreads = 128 + 128 * kGroups;
+constexpr int kSoft = 8;                              // first softmax warp
+constexpr int kThreads = 32 * kSoft + 128 * kGroups;
+constexpr int kLaunchRegs = 96;                       // registers a thread is launched with
+constexpr int kRegsIssue = 40, kRegsWiden = 56, kRegsSoft = 128;
+static_assert(kRegsIssue + kRegsWiden + kGroups * kRegsSoft == kThreads / 128 * kLaunchRegs, "register shares");
 constexpr int kRows = 128;
 constexpr int kChunk = 64;
 constexpr int kD = 128;
@@ -75,7 +83,7 @@ struct Layout {
 
 __host__ __device__ inline uint32_t al16(uint32_t x) { return (x + 15u) & ~15u; }
 
-enum : int { K_LAND = 0, S_FREE = 2, QK_DONE = 4, V8_LAND = 6, V8_FREE = 8, PV_READY = 10, PV_DONE = 12, O_FULL = 14, MMA_DONE = 15, N_BARS = 17 };
+enum : int { K_LAND = 0, S_FREE = 2, QK_DONE = 4, V8_LAND = 6, V8_FREE = 8, V16_READY = 10, PV_READY = 12, PV_DONE = 14, MMA_DONE = 16, O_FULL = 18, N_BARS = 19 };
 
 __host__ __device__ inline Layout make_layout(int k, int nwords, int BQ)
 {
@@ -156,7 +164,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(BAR(S_FREE + s), 8);
             mbar_init(BAR(QK_DONE + s), 1);
             mbar_init(BAR(V8_LAND + s), 1);
-            mbar_init(BAR(V8_FREE + s), 8);
+            mbar_init(BAR(V8_FREE + s), 4);
+            mbar_init(BAR(V16_READY + s), 4);
             mbar_init(BAR(PV_READY + s), 8);
             mbar_init(BAR(PV_DONE + s), 1);
             mbar_init(BAR(MMA_DONE + s), 1);
@@ -171,36 +180,47 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_alloc(smem_addr(tmem_holder), kTmemCols);
         tmem_relinquish();
     }
+    // every global load of the set-up is in flight before the first is used: the block's query rows (eight a warp, four
+    // elements a lane), its selection and its scores
+    uint2 v[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const int r = 8 * warp + i, qi = r / G, h = r % G;
+        v[i] = make_uint2(0u, 0u);
+        if (r < kRows && qi < nq) v[i] = __ldg(reinterpret_cast<const uint2 *>(Q + ((bg * G + h) * p.N + q0 + qi) * kD) + lane);
+    }
     for (int i = tid; i < nwords; i += kThreads) bitmap[i] = 0u;
     const int32_t *sel_base = sel_idx + (bg * p.N + q0) * p.k;
+#pragma unroll 4
     for (int e = tid; e < nq * p.k; e += kThreads) selbuf[e] = __ldg(sel_base + e);
+#pragma unroll 4
     for (int e = tid; e < G * nq * ns; e += kThreads) {
-        const int h = e / (nq * ns), rem = e % (nq * ns);
-        const size_t row0 = (bg * G + h) * p.N + q0;
-        wts[((rem / ns) * G + h) * ns + rem % ns] = __ldg(sel_score + row0 * ns + rem);
+        const int h = e / (nq * ns), rem = e - h * (nq * ns), qi = rem / ns;
+        wts[(qi * G + h) * ns + rem - qi * ns] = __ldg(sel_score + (bg * G + h) * p.N * ns + (size_t)q0 * ns + rem);
     }
-    // the query rows: a warp a row, four elements a lane, as two e4m3 tiles with the 128-byte swizzle
-    for (int r = warp; r < kRows; r += kThreads / 32) {
-        const int qi = r / G, h = r % G;
-        float x[4] = {0.f, 0.f, 0.f, 0.f};
-        if (qi < nq) {
-            const uint2 v = __ldg(reinterpret_cast<const uint2 *>(Q + ((bg * G + h) * p.N + q0 + qi) * kD) + lane);
-            x[0] = __uint_as_float(v.x << 16); x[1] = __uint_as_float(v.x & 0xFFFF0000u);
-            x[2] = __uint_as_float(v.y << 16); x[3] = __uint_as_float(v.y & 0xFFFF0000u);
-        }
-        const float m = warp_max(fmaxf(fmaxf(fabsf(x[0]), fabsf(x[1])), fmaxf(fabsf(x[2]), fabsf(x[3]))));
-        const int sh = min(7 - ((int)(__float_as_uint(m) >> 23) - 127), 120);
-        const float f = exp2_int(sh);
-        float rest[4];
+    // the query rows as two e4m3 tiles with the 128-byte swizzle
+    if (warp < kRows / 8) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) x[i] *= f;
-        const uint32_t hi = to_e4m3x4(x[0], x[1], x[2], x[3]);
-        e4m3x4_to_float(hi, rest);
-        const uint32_t lo = to_e4m3x4(x[0] - rest[0], x[1] - rest[1], x[2] - rest[2], x[3] - rest[3]);
-        const uint32_t at = (uint32_t)r * 128u + ((uint32_t)((lane >> 2) ^ (r & 7)) << 4) + (uint32_t)(lane & 3) * 4u;
-        *reinterpret_cast<uint32_t *>(base + Ly.q + at) = hi;
-        *reinterpret_cast<uint32_t *>(base + Ly.q + kQTile + at) = lo;
-        if (lane == 0) fqs[r] = p.scale * 1.4426950408889634f * exp2_int(-sh);
+        for (int i = 0; i < 8; ++i) {
+            const int r = 8 * warp + i;
+            float x[4] = {__uint_as_float(v[i].x << 16), __uint_as_float(v[i].x & 0xFFFF0000u),
+                          __uint_as_float(v[i].y << 16), __uint_as_float(v[i].y & 0xFFFF0000u)};
+            // the largest magnitude's bits: one integer reduction over the warp
+            const float m = __uint_as_float(__reduce_max_sync(
+                0xFFFFFFFFu, __float_as_uint(fmaxf(fmaxf(fabsf(x[0]), fabsf(x[1])), fmaxf(fabsf(x[2]), fabsf(x[3]))))));
+            const int sh = min(7 - ((int)(__float_as_uint(m) >> 23) - 127), 120);
+            const float f = exp2_int(sh);
+            float rest[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) x[e] *= f;
+            const uint32_t hi = to_e4m3x4(x[0], x[1], x[2], x[3]);
+            e4m3x4_to_float(hi, rest);
+            const uint32_t lo = to_e4m3x4(x[0] - rest[0], x[1] - rest[1], x[2] - rest[2], x[3] - rest[3]);
+            const uint32_t at = (uint32_t)r * 128u + ((uint32_t)((lane >> 2) ^ (r & 7)) << 4) + (uint32_t)(lane & 3) * 4u;
+            *reinterpret_cast<uint32_t *>(base + Ly.q + at) = hi;
+            *reinterpret_cast<uint32_t *>(base + Ly.q + kQTile + at) = lo;
+            if (lane == 0) fqs[r] = p.scale * 1.4426950408889634f * exp2_int(-sh);
+        }
     }
     fence_proxy_async_smem();
     __syncthreads();
@@ -268,6 +288,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t tmem = *tmem_holder;
     const int n_union = *n_union_p, n_pairs = (n_union + 1) >> 1;
 
+    // the roles' register shares (whole warpgroups: warps 0..3, 4..7 and the softmax groups)
+    if (warp < 4) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsIssue));
+    else if (warp < kSoft) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsWiden));
+    else asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoft));
+
     if (warp < 2) {
         // ---------------- key (warp 0) and value (warp 1) tiles, two chunks per slot
         if (lane == 0) {
@@ -313,7 +338,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                                   dk + (uint64_t)(((s & 3) * 32u) >> 4), idesc, s > 0 ? 1u : 0u);
                     mma_commit(BAR(QK_DONE + sl));
                 } else {
-                    ok = mbar_wait(BAR(PV_READY + sl), ph, limit_ns, abort_flag, status);
+                    ok = mbar_wait(BAR(V16_READY + sl), ph, limit_ns, abort_flag, status) &&
+                         mbar_wait(BAR(PV_READY + sl), ph, limit_ns, abort_flag, status);
                     if (!ok) break;
                     tc_fence_after();
                     const uint32_t pa = tmem + kColP + (uint32_t)sl * 64u;
@@ -334,39 +360,102 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_drain(done, 0, kDrainNs);
         }
         __syncwarp();
+    } else if (warp < kSoft) {
+        // ---------------- value pairs to f16: 16 bytes (key row, d = 16 j ..) a step
+        const int th = tid - 128, j = th & 7;
+        for (int pr = 0; pr < n_pairs; ++pr) {
+            const int sl = pr & 1;
+            const uint32_t ph = (uint32_t)((pr >> 1) & 1);
+            if (!warp_wait(BAR(V8_LAND + sl), ph, limit_ns, abort_flag, status) ||
+                (pr >= 2 && !warp_wait(BAR(PV_DONE + sl), ph ^ 1u, limit_ns, abort_flag, status)))
+                break;
+            const int n_ch = (2 * pr + 1 < n_union) ? 2 : 1;
+            for (int x = 0; x < n_ch; ++x) {
+                const int left = t_end - uni[2 * pr + x] * kChunk;   // rows behind the last query become zeros
+                const unsigned char *src = base + Ly.v8 + sl * kPair8 + x * (kPair8 / 2);
+                unsigned char *dst = base + Ly.v16 + sl * kPair16 + x * 8192u + (j >> 2) * 16384u;
+                uint4 v[4];
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    const int row = (th + 128 * u) >> 3;
+                    v[u] = reinterpret_cast<const uint4 *>(src)[row * 8 + (j ^ (row & 7))];
+                }
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    const int row = (th + 128 * u) >> 3;
+                    if (row >= left) v[u] = make_uint4(0u, 0u, 0u, 0u);
+                    const uint4 a = make_uint4(e4m3x2_to_f16x2(v[u].x), e4m3x2_to_f16x2(v[u].x >> 16),
+                                               e4m3x2_to_f16x2(v[u].y), e4m3x2_to_f16x2(v[u].y >> 16));
+                    const uint4 z = make_uint4(e4m3x2_to_f16x2(v[u].z), e4m3x2_to_f16x2(v[u].z >> 16),
+                                               e4m3x2_to_f16x2(v[u].w), e4m3x2_to_f16x2(v[u].w >> 16));
+                    // the second half's odd pieces go first: eight lanes, eight bank groups
+                    const int e = (2 * j) & 7, odd = j >> 2;
+                    *reinterpret_cast<uint4 *>(dst + row * 128u + (((e + odd) ^ (row & 7)) << 4)) = odd ? z : a;
+                    *reinterpret_cast<uint4 *>(dst + row * 128u + (((e + 1 - odd) ^ (row & 7)) << 4)) = odd ? a : z;
+                }
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(BAR(V8_FREE + sl));
+                mbar_arrive(BAR(V16_READY + sl));
+            }
+        }
     } else {
         // ---------------- softmax groups (chunks round-robin) and epilogue
-        if (warp < 8) {
-            // weights of each row by slot (warps 4..7, a thread a row): w vs over the row's largest, times 2^14
-            const int r = tid - 128, qi = r / G;
-            if (qi < nq) {
+        {
+            // weights of each row by slot, eight lanes a row: w vs over the row's largest, times 2^14
+            const int l8 = lane & 7;
+            constexpr int S8 = (HILS_MAX_K + 8) / 8;   // slots a lane holds at most
+            auto max8 = [](float x) {
+#pragma unroll
+                for (int o = 4; o; o >>= 1) x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, o));
+                return x;
+            };
+            for (int r = 4 * (warp - kSoft) + (lane >> 3); r < kRows; r += 16 * kGroups) {   // the same count for every warp's lanes
+                const int qi = min(r / G, nq - 1);
                 float *sc = wts + r * ns;
                 const int *sl = selbuf + qi * p.k;
                 const float *sv = qvs + qi * ns;
-                float M = -INFINITY, Z = 0.f, top = 0.f;
-                for (int j = 0; j < ns; ++j) {
-                    if (j < p.k && sl[j] < 0) sc[j] = -INFINITY;   // no chunk, whatever its score
-                    M = fmaxf(M, sc[j]);
+                const bool live = r / G < nq;
+                float x[S8], M = -INFINITY, Z = 0.f, top = 0.f;
+#pragma unroll
+                for (int u = 0; u < S8; ++u) {
+                    const int j = l8 + 8 * u;
+                    x[u] = -INFINITY;
+                    if (8 * u < ns) {   // a slot without a chunk has no weight, whatever its score
+                        if (live && j < ns && (j == p.k || sl[j] >= 0)) x[u] = sc[j];
+                        M = fmaxf(M, x[u]);
+                    }
                 }
-                for (int j = 0; j < ns; ++j) {
-                    const float e = (sc[j] == -INFINITY) ? 0.f : __expf(sc[j] - M);
-                    Z += e;
-                    sc[j] = e;
-                }
+                M = max8(M);
+#pragma unroll
+                for (int u = 0; u < S8; ++u)
+                    if (8 * u < ns) {
+                        x[u] = (x[u] == -INFINITY) ? 0.f : __expf(x[u] - M);
+                        Z += x[u];
+                    }
+#pragma unroll
+                for (int o = 4; o; o >>= 1) Z += __shfl_xor_sync(0xFFFFFFFFu, Z, o);
                 const float iz = Z == 0.f ? 0.f : 1.0f / Z;
-                for (int j = 0; j < ns; ++j) {
-                    const float w = sc[j] == 0.f ? 0.f : sc[j] * iz * sv[j];
-                    top = fmaxf(top, w);
-                    sc[j] = w;
-                }
+#pragma unroll
+                for (int u = 0; u < S8; ++u)
+                    if (8 * u < ns) {
+                        const int j = l8 + 8 * u;
+                        x[u] = (x[u] == 0.f || j >= ns) ? 0.f : x[u] * iz * sv[j];
+                        top = fmaxf(top, x[u]);
+                    }
+                top = max8(top);
                 const float f = top > 0.f ? kTopW / top : 1.0f;
-                for (int j = 0; j < ns; ++j) sc[j] *= f;
-                tops[r] = top > 0.f ? top * (1.0f / kTopW) : 0.f;
+#pragma unroll
+                for (int u = 0; u < S8; ++u)
+                    if (l8 + 8 * u < ns) sc[l8 + 8 * u] = x[u] * f;
+                if (l8 == 0) tops[r] = top > 0.f ? top * (1.0f / kTopW) : 0.f;
             }
         }
-        // the softmax warps wait for the weights (named barrier 1: warps 4..15 only)
+        // the softmax warps wait for the weights (named barrier 1: theirs only)
         asm volatile("bar.sync 1, %0;" ::"r"(32 * 4 * kGroups) : "memory");
-        const int grp = (warp - 4) >> 2;
+        const int grp = (warp - kSoft) >> 2;
         const int qq = warp & 3;
         const int r = 32 * qq + lane, h = r % G, qi = r / G;
         const bool valid = qi < nq;
@@ -377,7 +466,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float *wr = wts + r * ns;
         const float fq = fqs[r];
         const uint32_t lane_off = (uint32_t)(32 * qq) << 16;
-        const int gt = 32 * qq + lane;   // thread of the group
         int ptr = 0;
         bool ok = true;
         for (int t = grp; t < n_union; t += kGroups) {
@@ -386,35 +474,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int c = uni[t];
             const float kc = __ldg(ksb + c);
             const int left = min(kChunk, t_end - c * kChunk);   // tokens of the chunk that any query of the block sees
-            if (pr >= 2 && !warp_wait(BAR(PV_DONE + sl), ph ^ 1u, limit_ns, abort_flag, status)) { ok = false; break; }
-            if (!warp_wait(BAR(V8_LAND + sl), ph, limit_ns, abort_flag, status)) { ok = false; break; }
-            {
-                // widen the value tile: 16 bytes (key row, d = 16 j ..) a step; rows behind the last query become zeros
-                const unsigned char *src = base + Ly.v8 + sl * kPair8 + (t & 1) * (kPair8 / 2);
-                unsigned char *dst = base + Ly.v16 + sl * kPair16 + (t & 1) * 8192u;
-                uint4 v[4];
-#pragma unroll
-                for (int u = 0; u < 4; ++u) {
-                    const int row = (gt + 128 * u) >> 3;
-                    v[u] = reinterpret_cast<const uint4 *>(src)[row * 8 + ((gt & 7) ^ (row & 7))];
-                }
-#pragma unroll
-                for (int u = 0; u < 4; ++u) {
-                    const int row = (gt + 128 * u) >> 3, j = gt & 7;
-                    if (row >= left) v[u] = make_uint4(0u, 0u, 0u, 0u);
-                    const uint4 a = make_uint4(e4m3x2_to_f16x2(v[u].x), e4m3x2_to_f16x2(v[u].x >> 16),
-                                               e4m3x2_to_f16x2(v[u].y), e4m3x2_to_f16x2(v[u].y >> 16));
-                    const uint4 z = make_uint4(e4m3x2_to_f16x2(v[u].z), e4m3x2_to_f16x2(v[u].z >> 16),
-                                               e4m3x2_to_f16x2(v[u].w), e4m3x2_to_f16x2(v[u].w >> 16));
-                    unsigned char *d0 = dst + (j >> 2) * 16384u + row * 128u;
-                    const int e = (2 * j) & 7, odd = j >> 2;   // the second half's odd pieces go first: eight lanes, eight banks
-                    *reinterpret_cast<uint4 *>(d0 + (((e + odd) ^ (row & 7)) << 4)) = odd ? z : a;
-                    *reinterpret_cast<uint4 *>(d0 + (((e + 1 - odd) ^ (row & 7)) << 4)) = odd ? a : z;
-                }
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(BAR(V8_FREE + sl));
-            }
             if (!warp_wait(BAR(QK_DONE + sl), ph, limit_ns, abort_flag, status)) { ok = false; break; }
             tc_fence_after();
             uint32_t sv[64];
@@ -438,6 +497,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                 for (int j = 0; j < 32; ++j) pk[j] = 0u;
             }
+            if (pr >= 2 && !warp_wait(BAR(PV_DONE + sl), ph ^ 1u, limit_ns, abort_flag, status)) { ok = false; break; }
             tmem_st32(tmem + lane_off + kColP + (uint32_t)sl * 64u + (uint32_t)(t & 1) * 32u, pk);
             tmem_wait_st();
             tc_fence_before();
@@ -503,6 +563,12 @@ cudaError_t launch_g(const Dims &p, const void *Q, const uint8_t *K8, const uint
     const int c_max = (int)(((long long)p.q_offset + p.N - 1) / kChunk);
     const uint32_t smem = smem_bytes(p);
     auto kern = attend8_tc_kernel<G>;
+    // the warps' register shares are drawn from what the block is launched with: a build with fewer would wait forever
+    static const int regs = [] {
+        cudaFuncAttributes a;
+        return cudaFuncGetAttributes(&a, attend8_tc_kernel<G>) == cudaSuccess ? a.numRegs : -1;
+    }();
+    if (regs != kLaunchRegs) return cudaErrorInvalidConfiguration;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
     kern<<<dim3((p.N + BQ - 1) / BQ, p.Hkv, p.B), kThreads, smem, s>>>(
