@@ -26,6 +26,7 @@
 //
 // A row's slots are split over the warps of one block or of a cluster of blocks, and the partial rows meet in shared
 // memory (distributed shared memory for a cluster): no workspace, no atomics, a fixed order.
+#include <math.h>
 #include <stdlib.h>
 #include <string.h>
 #include <type_traits>
@@ -61,7 +62,8 @@ __device__ __forceinline__ float ld_cluster(uint32_t addr, uint32_t rank)
 // Blocks an SM holds, by the registers a thread needs.
 constexpr int blocks_per_sm(int D, int C, bool wide_q) { return D == 64 ? 4 : (C == 128 || wide_q) ? 2 : 3; }
 
-template <typename Tin, typename Tout, int D, int C>
+// SOLO: every warp has a row of work to itself; otherwise the warps of a block, or of a cluster of cs blocks, share one.
+template <typename Tin, typename Tout, int D, int C, bool SOLO>
 __global__ void __launch_bounds__(32 * kWarps, blocks_per_sm(D, C, sizeof(Tin) == 4))
     attend8_kernel(Dims p, int cs, int hgs, const Tin *__restrict__ Q, const uint8_t *__restrict__ K8,
                    const uint8_t *__restrict__ V8, const float *__restrict__ ks, const float *__restrict__ vs,
@@ -69,18 +71,23 @@ __global__ void __launch_bounds__(32 * kWarps, blocks_per_sm(D, C, sizeof(Tin) =
 {
     constexpr bool QHL = sizeof(Tin) == 4, PHL = sizeof(Tout) == 4;
     constexpr int MT = C / 16, KS = D / 16, DT = D / 16, WORDS = D / 8;
-    __shared__ float s_part[kWarps][kHeads][D + 4];   // + 4: the eight head rows of a fragment store on distinct banks
-    __shared__ float s_w[kHeads][kMaxSlots];
-    __shared__ float s_top[kHeads];
-    __shared__ int s_chunk[kMaxSlots];
+    constexpr int ROWS = SOLO ? kWarps : 1;           // rows of work a block has
+    __shared__ float s_part[SOLO ? 1 : kWarps][kHeads][D + 4];   // + 4: a fragment's eight head rows on distinct banks
+    __shared__ float s_weights[ROWS][kHeads][kMaxSlots];
+    __shared__ float s_tops[ROWS][kHeads];
+    __shared__ int s_chunks[ROWS][kMaxSlots];
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, r = lane >> 2, t = lane & 3;
-    const int rank = cs > 1 ? (int)cluster_rank() : 0;
-    const int unit = blockIdx.x / cs, i = unit / hgs;
+    const int rank = !SOLO && cs > 1 ? (int)cluster_rank() : 0;
+    const int unit = SOLO ? blockIdx.x * kWarps + warp : blockIdx.x / cs, i = unit / hgs;
+    if (SOLO && i >= p.N) return;                     // whole warps leave; a block of lone warps has no barrier
+    float (&s_w)[kHeads][kMaxSlots] = s_weights[SOLO ? warp : 0];
+    float (&s_top)[kHeads] = s_tops[SOLO ? warp : 0];
+    int (&s_chunk)[kMaxSlots] = s_chunks[SOLO ? warp : 0];
     const size_t bg = blockIdx.y;
     const int h0 = (unit % hgs) * kHeads, nh = min(p.G - h0, kHeads);
     const long long pos = (long long)p.q_offset + i;
-    const int ci = (int)(pos / C), ns = p.k + 1, nw = kWarps * cs, me = rank * kWarps + warp;
+    const int ci = (int)(pos / C), ns = p.k + 1, nw = SOLO ? 1 : kWarps * cs, me = SOLO ? 0 : rank * kWarps + warp;
     const int32_t *si = sel_idx + (bg * p.N + i) * p.k;
     const uint8_t *Kb = K8 + bg * (size_t)p.T * D + 16 * t;
     const uint8_t *Vb = V8 + bg * (size_t)p.T * D + (D / 8) * r;
@@ -143,13 +150,17 @@ __global__ void __launch_bounds__(32 * kWarps, blocks_per_sm(D, C, sizeof(Tin) =
     const float fq0 = __shfl_sync(0xFFFFFFFFu, fq, 8 * t), fq1 = __shfl_sync(0xFFFFFFFFu, fq, 8 * t + 4);
 
     // slot factors w_c vs_c over the row's largest, times 2^14; a slot without a chunk has no weight, whatever its score
-    for (int h = warp; h < kHeads; h += kWarps) {
+    for (int h = SOLO ? 0 : warp; h < kHeads; h += SOLO ? 1 : kWarps) {
+        if (h >= nh) {   // columns without a head: no weight
+            for (int jj = lane; jj < ns; jj += 32) s_w[h][jj] = 0.f;
+            continue;
+        }
         float s[3], v[3], mx = -INFINITY, z = 0.f, top = 0.f;
 #pragma unroll
         for (int u = 0; u < 3; ++u) {
             const int jj = lane + 32 * u;
             const int cc = chunk_of(jj);
-            s[u] = (cc >= 0 && h < nh) ? __ldg(sel_score + ((bg * p.G + h0 + h) * p.N + i) * ns + jj) : -INFINITY;
+            s[u] = cc >= 0 ? __ldg(sel_score + ((bg * p.G + h0 + h) * p.N + i) * ns + jj) : -INFINITY;
             v[u] = cc >= 0 ? __ldg(vs + bg * p.nL + cc) : 0.f;
             if (h == 0 && jj < ns) s_chunk[jj] = cc;
             mx = fmaxf(mx, s[u]);
@@ -174,7 +185,8 @@ __global__ void __launch_bounds__(32 * kWarps, blocks_per_sm(D, C, sizeof(Tin) =
             if (lane + 32 * u < ns) s_w[h][lane + 32 * u] = s[u] * f;
         if (lane == 0) s_top[h] = top > 0.f ? top * (1.0f / 16384.0f) : 0.f;
     }
-    __syncthreads();
+    if constexpr (SOLO) __syncwarp();
+    else __syncthreads();
 
     float oacc[DT][4];
 #pragma unroll
@@ -291,62 +303,98 @@ __global__ void __launch_bounds__(32 * kWarps, blocks_per_sm(D, C, sizeof(Tin) =
         c = cn;
     }
 
-    // the warps' rows meet: tile a, row r is d = (D / 8) r + 2 a, row r + 8 the next one; columns are heads 2t, 2t + 1
+    if constexpr (SOLO) {
+        // tile a, row r is d = (D / 8) r + 2 a, row r + 8 the next one; columns are heads 2t, 2t + 1
 #pragma unroll
-    for (int a = 0; a < DT; ++a) {
-        const int x = (D / 8) * r + 2 * a;
-        *reinterpret_cast<float2 *>(&s_part[warp][2 * t][x]) = make_float2(oacc[a][0], oacc[a][2]);
-        *reinterpret_cast<float2 *>(&s_part[warp][2 * t + 1][x]) = make_float2(oacc[a][1], oacc[a][3]);
-    }
-    __syncthreads();
-    if (cs > 1) {
+        for (int q = 0; q < 2; ++q) {
+            const int h = 2 * t + q;
+            if (h < nh) {
+                const float f = s_top[h];
+                float v[2 * DT];
+#pragma unroll
+                for (int a = 0; a < DT; ++a) {
+                    v[2 * a] = oacc[a][q] * f;
+                    v[2 * a + 1] = oacc[a][2 + q] * f;
+                }
+                store_n<2 * DT>(O + ((bg * p.G + h0 + h) * p.N + i) * D + (D / 8) * r, v);
+            }
+        }
+    } else {
+        // the warps' rows meet: tile a, row r is d = (D / 8) r + 2 a, row r + 8 the next one; columns are heads 2t, 2t + 1
+#pragma unroll
+        for (int a = 0; a < DT; ++a) {
+            const int x = (D / 8) * r + 2 * a;
+            *reinterpret_cast<float2 *>(&s_part[warp][2 * t][x]) = make_float2(oacc[a][0], oacc[a][2]);
+            *reinterpret_cast<float2 *>(&s_part[warp][2 * t + 1][x]) = make_float2(oacc[a][1], oacc[a][3]);
+        }
+        __syncthreads();
+        if (cs > 1) {
+            for (int e = tid; e < nh * D; e += 32 * kWarps) {
+                const int h = e / D, x = e % D;
+                float a = s_part[0][h][x];
+#pragma unroll
+                for (int w = 1; w < kWarps; ++w) a += s_part[w][h][x];
+                s_part[0][h][x] = a;
+            }
+            cluster_sync();
+            for (int e = rank * 32 * kWarps + tid; e < nh * D; e += cs * 32 * kWarps) {
+                const int h = e / D, x = e % D;
+                const uint32_t addr = sm100::smem_addr(&s_part[0][h][x]);
+                float a = 0.f;
+                for (int k = 0; k < cs; ++k) a += ld_cluster(addr, (uint32_t)k);
+                store_out(O + ((bg * p.G + h0 + h) * p.N + i) * D + x, a * s_top[h]);
+            }
+            cluster_sync();   // the others' reads of this block's rows
+            return;
+        }
         for (int e = tid; e < nh * D; e += 32 * kWarps) {
             const int h = e / D, x = e % D;
             float a = s_part[0][h][x];
 #pragma unroll
             for (int w = 1; w < kWarps; ++w) a += s_part[w][h][x];
-            s_part[0][h][x] = a;
-        }
-        cluster_sync();
-        for (int e = rank * 32 * kWarps + tid; e < nh * D; e += cs * 32 * kWarps) {
-            const int h = e / D, x = e % D;
-            const uint32_t addr = sm100::smem_addr(&s_part[0][h][x]);
-            float a = 0.f;
-            for (int k = 0; k < cs; ++k) a += ld_cluster(addr, (uint32_t)k);
             store_out(O + ((bg * p.G + h0 + h) * p.N + i) * D + x, a * s_top[h]);
         }
-        cluster_sync();   // the others' reads of this block's rows
-        return;
-    }
-    for (int e = tid; e < nh * D; e += 32 * kWarps) {
-        const int h = e / D, x = e % D;
-        float a = s_part[0][h][x];
-#pragma unroll
-        for (int w = 1; w < kWarps; ++w) a += s_part[w][h][x];
-        store_out(O + ((bg * p.G + h0 + h) * p.N + i) * D + x, a * s_top[h]);
     }
 }
 
-// Blocks a row of work is split over (a cluster of up to 8): as many as the GPU holds at once, more would queue
-// behind the first ones; and no more than shorten the longest warp's list of chunks.
-int split_of(const Dims &p, int hgs, int per_sm)
+// How the rows are shared out: cs = 0: a warp a row (SOLO), else teams of cs blocks; and the time it is expected to
+// take, in the time of a warp's chunk (2.9 us with every SM full).  Weighed: a warp's turns of its row (the longest
+// list and the mean), the start and end of a row (3 chunks for a lone warp, 1.5 for a team, its merge included), and how
+// often the resident warps start over.  8 rows of 65 slots go to teams of eight blocks (11.3 us; six 12.3, four 15.7),
+// 128 rows of 33 slots to teams of three (20.5 us; two 23.8, four, which queue, 31), 4072 rows of 33 slots to single
+// blocks (303 us; lone warps 347), 65536 rows of 17 slots and 2006 rows of 5 to lone warps (2.18 ms and 12.8 us; blocks
+// 2.54 ms and 20.1 us).
+struct Share {
+    int cs;
+    double time;
+};
+
+Share share_of(const Dims &p, int per_sm)
 {
-    const long long rows = (long long)p.B * p.Hkv * hgs * p.N, slots = 148ll * per_sm;
-    int best = 1;
-    auto rounds = [&](int cs) { return (p.k + kWarps * cs) / (kWarps * cs); };
-    for (int cs = 2; cs <= 8 && rows * cs <= slots; ++cs)
-        if (rounds(cs) < rounds(best)) best = cs;
+    const double rows = (double)p.B * p.Hkv * ((p.G + kHeads - 1) / kHeads) * p.N, blocks = 148.0 * per_sm;
+    const int ns = p.k + 1;
+    auto rounds = [](double x) { return x <= 1.0 ? 1.0 : x <= 4.0 ? ceil(x) + 0.25 : x + 0.5; };
+    Share best = {0, rounds(rows / (blocks * kWarps)) * (ns + 3.0)};
+    for (int cs = 1; cs <= 8; ++cs) {
+        const int w = kWarps * cs;
+        const double turns = 0.5 * ((ns + w - 1) / w + (double)ns / w);
+        const double t = rounds(rows * cs / blocks) * (turns + 1.5);
+        if (t < best.time) best = {cs, t};
+    }
     return best;
 }
+
+int per_sm_of(const Dims &p, hils_dtype in) { return blocks_per_sm(p.d, p.C, in == HILS_F32); }
 
 template <typename Tin, typename Tout, int D, int C>
 cudaError_t launch_t(const Dims &p, const void *Q, const uint8_t *K8, const uint8_t *V8, const float *ks, const float *vs,
                      const int32_t *sel_idx, const float *sel_score, void *O, cudaStream_t s)
 {
     const int hgs = (p.G + kHeads - 1) / kHeads;
-    const int cs = split_of(p, hgs, blocks_per_sm(D, C, sizeof(Tin) == 4));
+    const int cs = share_of(p, blocks_per_sm(D, C, sizeof(Tin) == 4)).cs;
+    const long long units = (long long)p.N * hgs;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)((long long)p.N * hgs * cs), (unsigned)(p.B * p.Hkv));
+    cfg.gridDim = dim3((unsigned)(cs ? units * cs : (units + kWarps - 1) / kWarps), (unsigned)(p.B * p.Hkv));
     cfg.blockDim = dim3(32 * kWarps);
     cfg.stream = s;
     cudaLaunchAttribute at;
@@ -355,8 +403,9 @@ cudaError_t launch_t(const Dims &p, const void *Q, const uint8_t *K8, const uint
     at.val.clusterDim.y = at.val.clusterDim.z = 1;
     cfg.attrs = &at;
     cfg.numAttrs = cs > 1 ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, attend8_kernel<Tin, Tout, D, C>, p, cs, hgs, static_cast<const Tin *>(Q), K8, V8, ks, vs,
-                              sel_idx, sel_score, static_cast<Tout *>(O));
+    auto *kern = cs ? attend8_kernel<Tin, Tout, D, C, false> : attend8_kernel<Tin, Tout, D, C, true>;
+    return cudaLaunchKernelEx(&cfg, kern, p, cs, hgs, static_cast<const Tin *>(Q), K8, V8, ks, vs, sel_idx, sel_score,
+                              static_cast<Tout *>(O));
 }
 
 template <typename Tin, typename Tout>
@@ -381,7 +430,15 @@ static bool use_union(const Dims &p, hils_dtype in, hils_dtype out)
     const char *force = getenv("HILS_Q8_KERNEL");
     if (force && strcmp(force, "rows") == 0) return false;
     if (force && strcmp(force, "union") == 0) return true;
-    return p.N >= 64;
+    // The union's cost is known only for selections that have nothing to do with one another, its worst case: of V
+    // visible chunks a block's BQ queries then want V (1 - (1 - k / V)^BQ).  A chunk of it takes 0.8 us and a
+    // block's set-up 5 us (8K prefill, 62 chunks on average: 835 us against 2.18 ms by rows; 509 queries at 130K, 810 chunks
+    // a block of which a query wants 33: 474 us against 303).
+    const double BQ = 128 / p.G, V = (p.q_offset + 0.5 * p.N) / p.C + 1.0;
+    const double U = V * (1.0 - pow(1.0 - fmin(1.0, p.k / V), BQ)) + BQ / p.C + 1.0;
+    const double blocks = (double)p.B * p.Hkv * ((p.N + BQ - 1) / BQ) / 148.0;
+    const double t_union = (blocks <= 1.0 ? 1.0 : blocks + 0.5) * (5.0 + 0.8 * fmin(U, V + 1.0));
+    return t_union < 2.9 * share_of(p, per_sm_of(p, in)).time;
 }
 
 cudaError_t launch_attend8(const Dims &p, hils_dtype in, hils_dtype out, const void *Q, const uint8_t *K8,

@@ -46,29 +46,6 @@ __device__ __forceinline__ uint32_t rest_f16(float a, float b, uint32_t h)
     return pack_f16(a - y.x, b - y.y);
 }
 
-// N consecutive results (N = 8 or 16).
-template <int N>
-__device__ __forceinline__ void store_n(float *p, const float *v)
-{
-#pragma unroll
-    for (int i = 0; i < N; i += 4) *reinterpret_cast<float4 *>(p + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
-}
-template <int N>
-__device__ __forceinline__ void store_n(__nv_bfloat16 *p, const float *v)
-{
-#pragma unroll
-    for (int i = 0; i < N; i += 8) {
-        uint4 u;
-        uint32_t *w = reinterpret_cast<uint32_t *>(&u);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const __nv_bfloat162 x = __floats2bfloat162_rn(v[i + 2 * j], v[i + 2 * j + 1]);
-            w[j] = *reinterpret_cast<const uint32_t *>(&x);
-        }
-        *reinterpret_cast<uint4 *>(p + i) = u;
-    }
-}
-
 // PART: the one chunk that t_end ends inside; otherwise whole chunks.
 template <typename Tin, int D, int C, bool PART>
 __global__ void __launch_bounds__(32 * kWarps, kBlocksPerSm)

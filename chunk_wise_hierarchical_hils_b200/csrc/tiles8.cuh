@@ -8,6 +8,7 @@
 //            A fragments of a product over the rows
 #pragma once
 
+#include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <stdint.h>
 
@@ -77,6 +78,29 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi)
 }
 
 __device__ __forceinline__ float2 unpack_f16(uint32_t v) { return __half22float2(*reinterpret_cast<const __half2 *>(&v)); }
+
+// Stores N consecutive results (N = 8 or 16), 16-byte aligned.
+template <int N>
+__device__ __forceinline__ void store_n(float *p, const float *v)
+{
+#pragma unroll
+    for (int i = 0; i < N; i += 4) *reinterpret_cast<float4 *>(p + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+}
+template <int N>
+__device__ __forceinline__ void store_n(__nv_bfloat16 *p, const float *v)
+{
+#pragma unroll
+    for (int i = 0; i < N; i += 8) {
+        uint4 u;
+        uint32_t *w = reinterpret_cast<uint32_t *>(&u);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const __nv_bfloat162 x = __floats2bfloat162_rn(v[i + 2 * j], v[i + 2 * j + 1]);
+            w[j] = *reinterpret_cast<const uint32_t *>(&x);
+        }
+        *reinterpret_cast<uint4 *>(p + i) = u;
+    }
+}
 
 }  // namespace t8
 }  // namespace hils
