@@ -194,18 +194,14 @@ __global__ void __launch_bounds__(32 * kWarps, blocks_per_sm(D, C, sizeof(Tin) =
 #pragma unroll
         for (int e = 0; e < 4; ++e) oacc[a][e] = 0.f;
 
-    while (c >= 0) {
+    auto attend_chunk = [&](auto own_chunk) {   // the chunk of this turn, whose first four tiles are loaded or on their way
+        constexpr bool OWN = decltype(own_chunk)::value;
         // the next turn of this warp that holds a chunk
         int tn = turn, cn = -1;
         while (cn < 0 && tn + nw < ns) { tn += nw; cn = s_chunk[tn - 1]; }
-        const bool own = turn == 0;
         auto load_next = [&](int n) {
-            if (n < 2 * MT) {
-                if (own) load_tile(std::true_type(), n, c, own_top);
-                else load_tile(std::false_type(), n, c, C - 1);
-            } else if (cn >= 0) {
-                load_tile(std::false_type(), n - 2 * MT, cn, C - 1);
-            }
+            if (n < 2 * MT) load_tile(own_chunk, n, c, OWN ? own_top : C - 1);
+            else if (cn >= 0) load_tile(std::false_type(), n - 2 * MT, cn, C - 1);
         };
         const float kc = __ldg(ks + bg * p.nL + c);
         const float f0 = fq0 * kc, f1 = fq1 * kc;
@@ -234,22 +230,25 @@ __global__ void __launch_bounds__(32 * kWarps, blocks_per_sm(D, C, sizeof(Tin) =
 
         // softmax over the keys seen (rows r, r + 8 of each tile, then across the lanes of a column).  Rows of the own
         // chunk that the query does not see hold its last row again: they do not change the maximum and weigh nothing.
-        float m0 = -INFINITY, m1 = -INFINITY;
+        // The factors are not negative: the largest product is the largest logit.
+        float m0 = fmaxf(sacc[0][0], sacc[0][2]), m1 = fmaxf(sacc[0][1], sacc[0][3]);
 #pragma unroll
-        for (int m = 0; m < MT; ++m) {
-            m0 = fmaxf(m0, fmaxf(sacc[m][0] * f0, sacc[m][2] * f0));
-            m1 = fmaxf(m1, fmaxf(sacc[m][1] * f1, sacc[m][3] * f1));
+        for (int m = 1; m < MT; ++m) {
+            m0 = sm100::fmax3(m0, sacc[m][0], sacc[m][2]);
+            m1 = sm100::fmax3(m1, sacc[m][1], sacc[m][3]);
         }
 #pragma unroll
         for (int o = 4; o < 32; o <<= 1) {
             m0 = fmaxf(m0, __shfl_xor_sync(0xFFFFFFFFu, m0, o));
             m1 = fmaxf(m1, __shfl_xor_sync(0xFFFFFFFFu, m1, o));
         }
+        m0 *= f0;
+        m1 *= f1;
 #pragma unroll
         for (int m = 0; m < MT; ++m)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) sacc[m][e] = exp2f(fmaf(sacc[m][e], (e & 1) ? f1 : f0, (e & 1) ? -m1 : -m0));
-        if (own) {
+            for (int e = 0; e < 4; ++e) sacc[m][e] = sm100::ex2_approx(fmaf(sacc[m][e], (e & 1) ? f1 : f0, (e & 1) ? -m1 : -m0));
+        if constexpr (OWN) {
 #pragma unroll
             for (int m = 0; m < MT; ++m)
 #pragma unroll
@@ -267,8 +266,8 @@ __global__ void __launch_bounds__(32 * kWarps, blocks_per_sm(D, C, sizeof(Tin) =
             l0 += __shfl_xor_sync(0xFFFFFFFFu, l0, o);
             l1 += __shfl_xor_sync(0xFFFFFFFFu, l1, o);
         }
-        const int slot = own ? p.k : turn - 1;
-        const float g0 = s_w[2 * t][slot] / l0, g1 = s_w[2 * t + 1][slot] / l1;
+        const int slot = OWN ? p.k : turn - 1;
+        const float g0 = __fdividef(s_w[2 * t][slot], l0), g1 = __fdividef(s_w[2 * t + 1][slot], l1);   // 1 <= l <= C
 
         // values
 #pragma unroll
@@ -301,7 +300,9 @@ __global__ void __launch_bounds__(32 * kWarps, blocks_per_sm(D, C, sizeof(Tin) =
         }
         turn = tn;
         c = cn;
-    }
+    };
+    if (turn == 0) attend_chunk(std::true_type());
+    while (c >= 0) attend_chunk(std::false_type());
 
     if constexpr (SOLO) {
         // tile a, row r is d = (D / 8) r + 2 a, row r + 8 the next one; columns are heads 2t, 2t + 1

@@ -342,7 +342,7 @@ HILS_API hils_status hils_landmarks_q8(const hils_problem *p, const void *K8, co
  * arguments (also those of hils_score_select_window, on its k'), ownership and
  * errors.  A slot with sel_idx -1 is empty whatever its score, and a slot with
  * score -INFINITY has no weight; a row without any weight is zero.  The scales
- * may be any finite floats.  The result is defined when the bytes the call's
+ * may be any finite floats that are not negative.  The result is defined when the bytes the call's
  * queries may see (t < q_offset + N, in selected chunks) hold no NaN and the
  * products stay in float range; bytes behind them may be anything.
  * Precision: products accumulate in float32.
