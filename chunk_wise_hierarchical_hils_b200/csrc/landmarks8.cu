@@ -17,6 +17,7 @@
 // rounding (2^-9).  Sums are float32.
 #include "cache8.h"
 #include "common.cuh"
+#include "sm100.cuh"
 #include "tiles8.cuh"
 
 namespace hils {
@@ -105,10 +106,11 @@ __global__ void __launch_bounds__(32 * kWarps, kBlocksPerSm)
         {
             float u[4];
             widen4(ur, u);
-            const float m = warp_max(fmaxf(fmaxf(fabsf(u[0]), fabsf(u[1])), fmaxf(fabsf(u[2]), fabsf(u[3]))));
+            const float m = __uint_as_float(__reduce_max_sync(
+                0xFFFFFFFFu, __float_as_uint(fmaxf(fmaxf(fabsf(u[0]), fabsf(u[1])), fmaxf(fabsf(u[2]), fabsf(u[3]))))));
             const int sh = min(14 - ((int)(__float_as_uint(m) >> 23) - 127), 120);
             const float f = exp2_int(sh);
-            fu = scale * exp2_int(-sh) * sc;
+            fu = scale * 1.4426950408889634f * exp2_int(-sh) * sc;   // logits in powers of two
             const uint32_t h0 = pack_f16(u[0] * f, u[1] * f), h1 = pack_f16(u[2] * f, u[3] * f);
             __syncwarp();
             if (r < KS) {
@@ -148,7 +150,7 @@ __global__ void __launch_bounds__(32 * kWarps, kBlocksPerSm)
             }
         }
 
-        // p (unnormalised, at most 1), its sum z, and y = sum p ln p
+        // p (unnormalised, at most 1), its sum z, and y = sum p log2 p
         float mx = -INFINITY, z = 0.f, y = 0.f;
 #pragma unroll
         for (int m = 0; m < MT; ++m)
@@ -162,9 +164,9 @@ __global__ void __launch_bounds__(32 * kWarps, kBlocksPerSm)
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 const float d = x[m][h] - mx;
-                const float w = !PART || 16 * m + 8 * h + r < a.rows ? expf(d) : 0.f;
+                const float w = !PART || 16 * m + 8 * h + r < a.rows ? sm100::ex2_approx(d) : 0.f;
                 z += w;
-                y += w == 0.f ? 0.f : w * d;
+                y = fmaf(w, fmaxf(d, -200.0f), y);   // w is 0 there
                 x[m][h] = w;
             }
 #pragma unroll
@@ -185,11 +187,10 @@ __global__ void __launch_bounds__(32 * kWarps, kBlocksPerSm)
             uint32_t b[2];
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                const float v0 = __shfl_sync(0xFFFFFFFFu, x[m][h], 8 * t) * PTOP;
-                const float v1 = __shfl_sync(0xFFFFFFFFu, x[m][h], 8 * t + 4) * PTOP;
-                const uint32_t hi = pack_f16(v0, v1);
-                b[h] = r == 0 ? hi : 0u;
-                if constexpr (F32) b[h] = r == 1 ? rest_f16(v0, v1, hi) : b[h];
+                const float v = x[m][h] * PTOP;
+                uint32_t c = pack_f16(v, 0.f);
+                if constexpr (F32) c = pack_f16(v, v - unpack_f16(c).x);
+                b[h] = movmatrix_t(t == 0 ? c : 0u);
             }
             const uint32_t *v = buf[(MT + m) & 3];
 #pragma unroll
@@ -218,7 +219,7 @@ __global__ void __launch_bounds__(32 * kWarps, kBlocksPerSm)
             }
             store_n<2 * DT>(L + a.crow * D + (D / 8) * r, v);
         }
-        if (beta && lane == 0) beta[a.crow] = logf(z) - y * inv;
+        if (beta && lane == 0) beta[a.crow] = logf(z) - y * inv * 0.6931471805599453f;
         if (!more) return;
         unit += step;
         a = an;
