@@ -7,17 +7,14 @@
 // Every selected chunk is 2 C d bytes that one query group uses once, so the kernel's job is to keep loads in
 // flight; the products run on mma.sync tiles (4 heads x 64 keys x 128 columns is far below a tcgen05 tile).
 //
-// One warp takes a whole chunk at a time, straight from global memory into registers: no shared-memory tiles,
-// because e4m3 bytes have to pass through registers anyway to become f16 (exact), and because the index orders of an
-// mma product are free: the d index of Q K^T and the d rows of V^T P are permuted so that what a lane's 16-byte loads
-// bring is what its fragments hold.
-//   S^T = K Q^T     A = 16 keys x 16 of d, B = 8 heads: lane (r, t) = (lane / 4, lane % 4) loads 16 bytes of keys r
-//                   and r + 8 at d = 64 s + 16 t, whose words are its A fragments of four k-steps
-//   O^T = V^T P^T   A = 16 of d x 16 keys: the lane loads 16 bytes at d = 16 r of keys 2t, 2t+1, 2t+8, 2t+9; byte
-//                   permutes pair the keys; P^T comes from S^T's accumulators by movmatrix
-// The eight columns are heads: a group of more than eight is two rows of work.  While a chunk's probabilities are
-// made the next chunk's keys are on their way, and its values during the next chunk's scores, so a warp
-// keeps 8 to 16 KB in flight.
+// One warp takes a whole chunk at a time, on tiles of 16 keys in shared memory that it fills itself (tiles8.cuh):
+//   S^T = K Q^T     A = 16 keys x 16 of d, B = 8 heads
+//   O^T = V^T P^T   A = 16 of d x 16 keys (bytes transposed as they are read); P^T comes from S^T's accumulators by
+//                   movmatrix
+// e4m3 becomes f16 (exact) in registers.  The eight columns are heads: a group of more than eight is two rows of work.  A
+// chunk is a stream of pairs of tiles, its keys' and then its values', through a ring of up to four pairs: once a pair is
+// used its place is filled with the pair four further on, which runs on into the warp's next chunk, so a warp has
+// 8 to 16 KB in flight or in use.
 //
 // Numbers.  A query row is scaled by a power of two to just below 2^15 and taken in f16: bf16 queries keep their 8 bits down
 // to 2^-29 of the row's largest, and below that an error of 2^-39 of it; float32 queries are two f16 pieces (22 bits).
@@ -31,7 +28,7 @@
 #include <string.h>
 #include <type_traits>
 
-#include "attend_simt.cuh"
+#include "common.cuh"
 #include "cache8.h"
 #include "sm100.cuh"
 #include "tiles8.cuh"
@@ -59,20 +56,30 @@ __device__ __forceinline__ float ld_cluster(uint32_t addr, uint32_t rank)
     return v;
 }
 
-// Blocks an SM holds, by the registers a thread needs.
-constexpr int blocks_per_sm(int D, int C, bool wide_q) { return D == 64 ? 4 : (C == 128 || wide_q) ? 2 : 3; }
+// Blocks an SM holds: by registers, and for d = 128 by 16 KB of ring a warp.
+constexpr int blocks_per_sm(int D) { return D == 64 ? 4 : 3; }
+
+constexpr int ring_space(int D, int C)   // a warp's shared memory: its ring, later its partial rows
+{
+    const int ring = (C / 16 < 4 ? C / 16 : 4) * 32 * D, rows = (kHeads * (D + 4) * 4 + 127) / 128 * 128;
+    return ring > rows ? ring : rows;
+}
 
 // SOLO: every warp has a row of work to itself; otherwise the warps of a block, or of a cluster of cs blocks, share one.
 template <typename Tin, typename Tout, int D, int C, bool SOLO>
-__global__ void __launch_bounds__(32 * kWarps, blocks_per_sm(D, C, sizeof(Tin) == 4))
+__global__ void __launch_bounds__(32 * kWarps, blocks_per_sm(D))
     attend8_kernel(Dims p, int cs, int hgs, const Tin *__restrict__ Q, const uint8_t *__restrict__ K8,
                    const uint8_t *__restrict__ V8, const float *__restrict__ ks, const float *__restrict__ vs,
                    const int32_t *__restrict__ sel_idx, const float *__restrict__ sel_score, Tout *__restrict__ O)
 {
     constexpr bool QHL = sizeof(Tin) == 4, PHL = sizeof(Tout) == 4;
-    constexpr int MT = C / 16, KS = D / 16, DT = D / 16, WORDS = D / 8;
+    constexpr int MT = C / 16, KS = D / 16;
+    constexpr int NP = MT, RP = NP < 4 ? NP : 4;      // pairs of tiles a chunk is (half of them keys), pairs in a ring
+    constexpr int PAIR = 32 * D;
     constexpr int ROWS = SOLO ? kWarps : 1;           // rows of work a block has
-    __shared__ float s_part[SOLO ? 1 : kWarps][kHeads][D + 4];   // + 4: a fragment's eight head rows on distinct banks
+    constexpr int PITCH = D + 4;                      // of a row of partial results: lanes of a fragment on distinct banks
+    constexpr int SPACE = ring_space(D, C);
+    extern __shared__ __align__(128) unsigned char s_ring[];   // [warp][SPACE]: its ring, then its partial rows
     __shared__ float s_weights[ROWS][kHeads][kMaxSlots];
     __shared__ float s_tops[ROWS][kHeads];
     __shared__ int s_chunks[ROWS][kMaxSlots];
@@ -89,16 +96,15 @@ __global__ void __launch_bounds__(32 * kWarps, blocks_per_sm(D, C, sizeof(Tin) =
     const long long pos = (long long)p.q_offset + i;
     const int ci = (int)(pos / C), ns = p.k + 1, nw = SOLO ? 1 : kWarps * cs, me = SOLO ? 0 : rank * kWarps + warp;
     const int32_t *si = sel_idx + (bg * p.N + i) * p.k;
-    const uint8_t *Kb = K8 + bg * (size_t)p.T * D + 16 * t;
-    const uint8_t *Vb = V8 + bg * (size_t)p.T * D + (D / 8) * r;
+    const uint8_t *Kb = K8 + bg * (size_t)p.T * D, *Vb = V8 + bg * (size_t)p.T * D;
+    const uint32_t ring = sm100::smem_addr(s_ring) + (uint32_t)warp * SPACE;
+    float *part = reinterpret_cast<float *>(s_ring + warp * SPACE);   // [head][PITCH]
 
-    // A chunk is a stream of 2 MT tiles, its keys' and then its values', through four register buffers: once tile n
-    // is used, its buffer is loaded with tile n + 4 of the stream, which runs on into the warp's next chunk.
-    uint32_t buf[4][WORDS];
-    auto load_tile = [&](auto part, int n, int c, int top) {   // tile n of chunk c, whose last row seen is `top`
-        constexpr bool PART = decltype(part)::value;
-        if (n < MT) load_k<D, PART>(buf[n & 3], Kb + ((size_t)c * C + 16 * n) * D, r, top - 16 * n);
-        else load_v<D, PART>(buf[n & 3], Vb + ((size_t)c * C + 16 * (n - MT)) * D, t, top - 16 * (n - MT));
+    auto load_pair = [&](auto part_chunk, int n, int c, int top) {   // pair n of chunk c, whose last row seen is `top`
+        constexpr bool PART = decltype(part_chunk)::value;
+        const int row = 32 * (n < NP / 2 ? n : n - NP / 2);
+        load_rows<D, 32, PART>(ring + (uint32_t)(n % RP) * PAIR, (n < NP / 2 ? Kb : Vb) + ((size_t)c * C + row) * D, top - row);
+        cp_commit();
     };
 
     // The own chunk, whose rows behind the query are not seen, is the first in the order of work and past chunks (whole
@@ -109,40 +115,37 @@ __global__ void __launch_bounds__(32 * kWarps, blocks_per_sm(D, C, sizeof(Tin) =
     const int own_top = (int)(pos - (long long)ci * C);
     if (turn == 0) {
 #pragma unroll
-        for (int n = 0; n < 4; ++n) load_tile(std::true_type(), n, c, own_top);
+        for (int n = 0; n < RP; ++n) load_pair(std::true_type(), n, c, own_top);
     } else if (c >= 0) {
 #pragma unroll
-        for (int n = 0; n < 4; ++n) load_tile(std::false_type(), n, c, C - 1);
+        for (int n = 0; n < RP; ++n) load_pair(std::false_type(), n, c, C - 1);
     }
 
-    // the query rows: lane (r, t) holds head h0 + r at d = 64 s + 16 t .. + 15
+    // the query rows: lane (r, t) holds head h0 + r at d = 16 c + 4 t .. + 3
     uint32_t qh[KS][2], ql[QHL ? KS : 1][2];
     float fq;   // scale log2(e) / the row's power of two, for head r
     {
-        float x[D / 64][16], m = 0.f;
-        const Tin *qr = Q + ((bg * p.G + h0 + min(r, nh - 1)) * p.N + i) * D + 16 * t;
+        float x[KS][4], m = 0.f;
+        const Tin *qr = Q + ((bg * p.G + h0 + min(r, nh - 1)) * p.N + i) * D + 4 * t;
 #pragma unroll
-        for (int s = 0; s < D / 64; ++s) {
-            load8(qr + 64 * s, x[s]);
-            load8(qr + 64 * s + 8, x[s] + 8);
+        for (int c16 = 0; c16 < KS; ++c16) load4(qr + 16 * c16, x[c16]);
 #pragma unroll
-            for (int e = 0; e < 16; ++e) m = fmaxf(m, fabsf(x[s][e]));
-        }
+        for (int c16 = 0; c16 < KS; ++c16)
+            m = fmaxf(m, fmaxf(fmaxf(fabsf(x[c16][0]), fabsf(x[c16][1])), fmaxf(fabsf(x[c16][2]), fabsf(x[c16][3]))));
         m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
         m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
         const int sh = min(14 - ((int)(__float_as_uint(m) >> 23) - 127), 120);
         const float f = exp2_int(sh);
         fq = p.scale * 1.4426950408889634f * exp2_int(-sh);
 #pragma unroll
-        for (int s = 0; s < D / 64; ++s)
+        for (int c16 = 0; c16 < KS; ++c16)
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const float a = x[s][2 * e] * f, b = x[s][2 * e + 1] * f;
-                const uint32_t v = pack_f16(a, b);
-                qh[4 * s + e / 2][e & 1] = v;
+            for (int e = 0; e < 2; ++e) {
+                const float a = x[c16][2 * e] * f, b = x[c16][2 * e + 1] * f;
+                qh[c16][e] = pack_f16(a, b);
                 if constexpr (QHL) {
-                    const float2 y = unpack_f16(v);
-                    ql[4 * s + e / 2][e & 1] = pack_f16(a - y.x, b - y.y);
+                    const float2 y = unpack_f16(qh[c16][e]);
+                    ql[c16][e] = pack_f16(a - y.x, b - y.y);
                 }
             }
     }
@@ -188,20 +191,26 @@ __global__ void __launch_bounds__(32 * kWarps, blocks_per_sm(D, C, sizeof(Tin) =
     if constexpr (SOLO) __syncwarp();
     else __syncthreads();
 
-    float oacc[DT][4];
+    float oacc[KS][4];   // tile c, rows r and r + 8: d = 16 c + r (+ 8); columns are heads 2t, 2t + 1
 #pragma unroll
-    for (int a = 0; a < DT; ++a)
+    for (int a = 0; a < KS; ++a)
 #pragma unroll
         for (int e = 0; e < 4; ++e) oacc[a][e] = 0.f;
 
-    auto attend_chunk = [&](auto own_chunk) {   // the chunk of this turn, whose first four tiles are loaded or on their way
+    auto attend_chunk = [&](auto own_chunk) {   // the chunk of this turn, whose first pairs of tiles are on their way
         constexpr bool OWN = decltype(own_chunk)::value;
         // the next turn of this warp that holds a chunk
         int tn = turn, cn = -1;
         while (cn < 0 && tn + nw < ns) { tn += nw; cn = s_chunk[tn - 1]; }
-        auto load_next = [&](int n) {
-            if (n < 2 * MT) load_tile(own_chunk, n, c, OWN ? own_top : C - 1);
-            else if (cn >= 0) load_tile(std::false_type(), n - 2 * MT, cn, C - 1);
+        // use(n, f): f on pair n of the stream once it is there; then its place is filled with the pair RP further on
+        auto use = [&](int n, auto f) {
+            cp_wait<RP - 1>();
+            __syncwarp();
+            f(ring + (uint32_t)(n % RP) * PAIR);
+            __syncwarp();
+            if (n + RP < NP) load_pair(own_chunk, n + RP, c, OWN ? own_top : C - 1);
+            else if (cn >= 0) load_pair(std::false_type(), n + RP - NP, cn, C - 1);
+            else cp_commit();   // groups are counted
         };
         const float kc = __ldg(ks + bg * p.nL + c);
         const float f0 = fq0 * kc, f1 = fq1 * kc;
@@ -209,26 +218,24 @@ __global__ void __launch_bounds__(32 * kWarps, blocks_per_sm(D, C, sizeof(Tin) =
         // scores, two tiles of keys at a time: their products are independent of one another
         float sacc[MT][4];
 #pragma unroll
-        for (int m = 0; m < MT; m += 2) {
-#pragma unroll
-            for (int e = 0; e < 4; ++e) sacc[m][e] = sacc[m + 1][e] = 0.f;
-#pragma unroll
-            for (int kk = 0; kk < KS; ++kk) {
+        for (int m = 0; m < MT; m += 2)
+            use(m / 2, [&](uint32_t tile) {
+                uint32_t w[2][KS][2];
 #pragma unroll
                 for (int u = 0; u < 2; ++u) {
-                    const uint32_t *w = buf[(m + u) & 3];
-                    const uint32_t w0 = w[kk], w1 = w[KS + kk];
-                    const uint32_t a0 = e4m3x2_to_f16x2(w0), a1 = e4m3x2_to_f16x2(w1);
-                    const uint32_t a2 = e4m3x2_to_f16x2(w0 >> 16), a3 = e4m3x2_to_f16x2(w1 >> 16);
-                    mma_f16(sacc[m + u], a0, a1, a2, a3, qh[kk][0], qh[kk][1]);
-                    if constexpr (QHL) mma_f16(sacc[m + u], a0, a1, a2, a3, ql[kk][0], ql[kk][1]);
+                    read_keys<D>(tile + u * 16 * D, w[u]);
+                    sacc[m + u][0] = sacc[m + u][1] = sacc[m + u][2] = sacc[m + u][3] = 0.f;
                 }
-            }
 #pragma unroll
-            for (int u = 0; u < 2; ++u) load_next(m + u + 4);
-        }
+                for (int k = 0; k < KS; ++k)
+#pragma unroll
+                    for (int u = 0; u < 2; ++u) {
+                        mma_bytes(sacc[m + u], w[u][k][0], w[u][k][1], qh[k][0], qh[k][1]);
+                        if constexpr (QHL) mma_bytes(sacc[m + u], w[u][k][0], w[u][k][1], ql[k][0], ql[k][1]);
+                    }
+            });
 
-        // softmax over the keys seen (rows r, r + 8 of each tile, then across the lanes of a column).  Rows of the own
+        // softmax over the keys seen (those of rows r, r + 8 of each tile, then across the lanes of a column).  Rows of the own
         // chunk that the query does not see hold its last row again: they do not change the maximum and weigh nothing.
         // The factors are not negative: the largest product is the largest logit.
         float m0 = fmaxf(sacc[0][0], sacc[0][2]), m1 = fmaxf(sacc[0][1], sacc[0][3]);
@@ -253,7 +260,7 @@ __global__ void __launch_bounds__(32 * kWarps, blocks_per_sm(D, C, sizeof(Tin) =
             for (int m = 0; m < MT; ++m)
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
-                    if (16 * m + 8 * (e >> 1) + r > own_top) sacc[m][e] = 0.f;
+                    if (16 * m + key_row(r, e >> 1) > own_top) sacc[m][e] = 0.f;
         }
         float l0 = 0.f, l1 = 0.f;
 #pragma unroll
@@ -271,76 +278,68 @@ __global__ void __launch_bounds__(32 * kWarps, blocks_per_sm(D, C, sizeof(Tin) =
 
         // values
 #pragma unroll
-        for (int m = 0; m < MT; ++m) {
-            const float(&e)[4] = sacc[m];
-            const uint32_t *vw = buf[(MT + m) & 3];
-            const float x0 = e[0] * g0, x1 = e[1] * g1, x2 = e[2] * g0, x3 = e[3] * g1;
-            const uint32_t pa = pack_f16(x0, x1), pb = pack_f16(x2, x3);
-            const uint32_t b0 = movmatrix_t(pa), b1 = movmatrix_t(pb);
-            uint32_t c0 = 0u, c1 = 0u;
-            if constexpr (PHL) {
-                const float2 ya = unpack_f16(pa), yb = unpack_f16(pb);
-                c0 = movmatrix_t(pack_f16(x0 - ya.x, x1 - ya.y));
-                c1 = movmatrix_t(pack_f16(x2 - yb.x, x3 - yb.y));
-            }
+        for (int m = 0; m < MT; m += 2)
+            use(NP / 2 + m / 2, [&](uint32_t tile) {
 #pragma unroll
-            for (int w = 0; w < D / 32; ++w) {
-                const uint32_t k0 = vw[w], k1 = vw[D / 32 + w], k8 = vw[2 * (D / 32) + w], k9 = vw[3 * (D / 32) + w];
+                for (int u = 0; u < 2; ++u) {
+                    const float(&e)[4] = sacc[m + u];
+                    const float x0 = e[0] * g0, x1 = e[1] * g1, x2 = e[2] * g0, x3 = e[3] * g1;
+                    const uint32_t pa = pack_f16(x0, x1), pb = pack_f16(x2, x3);
+                    const uint32_t b0 = movmatrix_t(pa), b1 = movmatrix_t(pb);
+                    [[maybe_unused]] uint32_t r0 = 0u, r1 = 0u;   // what f16 leaves of the probabilities
+                    if constexpr (PHL) {
+                        const float2 ya = unpack_f16(pa), yb = unpack_f16(pb);
+                        r0 = movmatrix_t(pack_f16(x0 - ya.x, x1 - ya.y));
+                        r1 = movmatrix_t(pack_f16(x2 - yb.x, x3 - yb.y));
+                    }
 #pragma unroll
-                for (int hw = 0; hw < 2; ++hw) {
-                    const uint32_t lo = __byte_perm(k0, k1, hw ? 0x7362 : 0x5140);
-                    const uint32_t hi = __byte_perm(k8, k9, hw ? 0x7362 : 0x5140);
-                    const uint32_t a0 = e4m3x2_to_f16x2(lo), a1 = e4m3x2_to_f16x2(lo >> 16);
-                    const uint32_t a2 = e4m3x2_to_f16x2(hi), a3 = e4m3x2_to_f16x2(hi >> 16);
-                    mma_f16(oacc[2 * w + hw], a0, a1, a2, a3, b0, b1);
-                    if constexpr (PHL) mma_f16(oacc[2 * w + hw], a0, a1, a2, a3, c0, c1);
+                    for (int k = 0; k < KS; k += 2) {
+                        uint32_t w[2][2];
+                        read_values<D>(tile + u * 16 * D, k, w);
+#pragma unroll
+                        for (int v = 0; v < 2; ++v) {
+                            mma_bytes(oacc[k + v], w[v][0], w[v][1], b0, b1);
+                            if constexpr (PHL) mma_bytes(oacc[k + v], w[v][0], w[v][1], r0, r1);
+                        }
+                    }
                 }
-            }
-            load_next(MT + m + 4);
-        }
+            });
         turn = tn;
         c = cn;
     };
     if (turn == 0) attend_chunk(std::true_type());
     while (c >= 0) attend_chunk(std::false_type());
 
+    // the rows of partial results take the ring's place (nothing is on its way into it any more)
+    __syncwarp();
+#pragma unroll
+    for (int a = 0; a < KS; ++a)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) part[(2 * t + (e & 1)) * PITCH + 16 * a + r + 8 * (e >> 1)] = oacc[a][e];
     if constexpr (SOLO) {
-        // tile a, row r is d = (D / 8) r + 2 a, row r + 8 the next one; columns are heads 2t, 2t + 1
-#pragma unroll
-        for (int q = 0; q < 2; ++q) {
-            const int h = 2 * t + q;
-            if (h < nh) {
-                const float f = s_top[h];
-                float v[2 * DT];
-#pragma unroll
-                for (int a = 0; a < DT; ++a) {
-                    v[2 * a] = oacc[a][q] * f;
-                    v[2 * a + 1] = oacc[a][2 + q] * f;
-                }
-                store_n<2 * DT>(O + ((bg * p.G + h0 + h) * p.N + i) * D + (D / 8) * r, v);
-            }
+        __syncwarp();
+        for (int e = lane; e < nh * D / 4; e += 32) {
+            const int h = e / (D / 4), x = e % (D / 4) * 4;
+            const float4 v = *reinterpret_cast<const float4 *>(part + h * PITCH + x);
+            const float f = s_top[h];
+            store4(O + ((bg * p.G + h0 + h) * p.N + i) * D + x, make_float4(v.x * f, v.y * f, v.z * f, v.w * f));
         }
     } else {
-        // the warps' rows meet: tile a, row r is d = (D / 8) r + 2 a, row r + 8 the next one; columns are heads 2t, 2t + 1
-#pragma unroll
-        for (int a = 0; a < DT; ++a) {
-            const int x = (D / 8) * r + 2 * a;
-            *reinterpret_cast<float2 *>(&s_part[warp][2 * t][x]) = make_float2(oacc[a][0], oacc[a][2]);
-            *reinterpret_cast<float2 *>(&s_part[warp][2 * t + 1][x]) = make_float2(oacc[a][1], oacc[a][3]);
-        }
+        // the warps' rows, and a cluster's, are added in order
         __syncthreads();
+        float *sum = reinterpret_cast<float *>(s_ring);
         if (cs > 1) {
             for (int e = tid; e < nh * D; e += 32 * kWarps) {
-                const int h = e / D, x = e % D;
-                float a = s_part[0][h][x];
+                float *at = sum + e / D * PITCH + e % D;
+                float a = at[0];
 #pragma unroll
-                for (int w = 1; w < kWarps; ++w) a += s_part[w][h][x];
-                s_part[0][h][x] = a;
+                for (int w = 1; w < kWarps; ++w) a += at[w * (SPACE / 4)];
+                at[0] = a;
             }
             cluster_sync();
             for (int e = rank * 32 * kWarps + tid; e < nh * D; e += cs * 32 * kWarps) {
                 const int h = e / D, x = e % D;
-                const uint32_t addr = sm100::smem_addr(&s_part[0][h][x]);
+                const uint32_t addr = sm100::smem_addr(sum + h * PITCH + x);
                 float a = 0.f;
                 for (int k = 0; k < cs; ++k) a += ld_cluster(addr, (uint32_t)k);
                 store_out(O + ((bg * p.G + h0 + h) * p.N + i) * D + x, a * s_top[h]);
@@ -348,12 +347,17 @@ __global__ void __launch_bounds__(32 * kWarps, blocks_per_sm(D, C, sizeof(Tin) =
             cluster_sync();   // the others' reads of this block's rows
             return;
         }
-        for (int e = tid; e < nh * D; e += 32 * kWarps) {
-            const int h = e / D, x = e % D;
-            float a = s_part[0][h][x];
+        for (int e = tid; e < nh * D / 4; e += 32 * kWarps) {
+            const int h = e / (D / 4), x = e % (D / 4) * 4;
+            const float *at = sum + h * PITCH + x;
+            float4 a = *reinterpret_cast<const float4 *>(at);
 #pragma unroll
-            for (int w = 1; w < kWarps; ++w) a += s_part[w][h][x];
-            store_out(O + ((bg * p.G + h0 + h) * p.N + i) * D + x, a * s_top[h]);
+            for (int w = 1; w < kWarps; ++w) {
+                const float4 v = *reinterpret_cast<const float4 *>(at + w * (SPACE / 4));
+                a = make_float4(a.x + v.x, a.y + v.y, a.z + v.z, a.w + v.w);
+            }
+            const float f = s_top[h];
+            store4(O + ((bg * p.G + h0 + h) * p.N + i) * D + x, make_float4(a.x * f, a.y * f, a.z * f, a.w * f));
         }
     }
 }
@@ -385,18 +389,17 @@ Share share_of(const Dims &p, int per_sm)
     return best;
 }
 
-int per_sm_of(const Dims &p, hils_dtype in) { return blocks_per_sm(p.d, p.C, in == HILS_F32); }
-
 template <typename Tin, typename Tout, int D, int C>
 cudaError_t launch_t(const Dims &p, const void *Q, const uint8_t *K8, const uint8_t *V8, const float *ks, const float *vs,
                      const int32_t *sel_idx, const float *sel_score, void *O, cudaStream_t s)
 {
     const int hgs = (p.G + kHeads - 1) / kHeads;
-    const int cs = share_of(p, blocks_per_sm(D, C, sizeof(Tin) == 4)).cs;
+    const int cs = share_of(p, blocks_per_sm(D)).cs;
     const long long units = (long long)p.N * hgs;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(cs ? units * cs : (units + kWarps - 1) / kWarps), (unsigned)(p.B * p.Hkv));
     cfg.blockDim = dim3(32 * kWarps);
+    cfg.dynamicSmemBytes = kWarps * ring_space(D, C);
     cfg.stream = s;
     cudaLaunchAttribute at;
     at.id = cudaLaunchAttributeClusterDimension;
@@ -405,6 +408,8 @@ cudaError_t launch_t(const Dims &p, const void *Q, const uint8_t *K8, const uint
     cfg.attrs = &at;
     cfg.numAttrs = cs > 1 ? 1 : 0;
     auto *kern = cs ? attend8_kernel<Tin, Tout, D, C, false> : attend8_kernel<Tin, Tout, D, C, true>;
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)cfg.dynamicSmemBytes);
+    if (e != cudaSuccess) return e;
     return cudaLaunchKernelEx(&cfg, kern, p, cs, hgs, static_cast<const Tin *>(Q), K8, V8, ks, vs, sel_idx, sel_score,
                               static_cast<Tout *>(O));
 }
@@ -439,7 +444,7 @@ static bool use_union(const Dims &p, hils_dtype in, hils_dtype out)
     const double U = V * (1.0 - pow(1.0 - fmin(1.0, p.k / V), BQ)) + BQ / p.C + 1.0;
     const double blocks = (double)p.B * p.Hkv * ((p.N + BQ - 1) / BQ) / 148.0;
     const double t_union = (blocks <= 1.0 ? 1.0 : blocks + 0.5) * (5.0 + 0.8 * fmin(U, V + 1.0));
-    return t_union < 2.9 * share_of(p, per_sm_of(p, in)).time;
+    return t_union < 2.9 * share_of(p, blocks_per_sm(p.d)).time;
 }
 
 cudaError_t launch_attend8(const Dims &p, hils_dtype in, hils_dtype out, const void *Q, const uint8_t *K8,

@@ -5,11 +5,10 @@
 // scale) the logits are scale s_c <u, e_t>, the landmark is s_c sum_t p_t e_t, and the entropy of p is the chunk's
 // bias.
 //
-// Every key byte is read once from HBM and used in two products, so the kernel is bound by HBM as long as the
-// products stay cheap: one warp per chunk, mma.sync tiles of f16 (e4m3 is exact in it), with the pipeline of the
-// attention kernel: a chunk is a stream of tiles, as keys (for the logits) and again as values (for the sum; these
-// loads hit L1), through four register buffers, running on into the warp's next chunk.  (mma.sync has an e4m3 form, but
-// on this GPU it runs as conversions and two f16 products: 1134 instructions a chunk against 828 in this form.)
+// Every key byte is read once from HBM and used in two products (logits, sum), so the kernel is bound by HBM as long as
+// the products stay cheap: one warp per chunk, mma.sync tiles of f16 (e4m3 is exact in it) read from two chunk buffers
+// in shared memory, one in use and one being filled.  (mma.sync has an e4m3 form, but on this GPU it runs as
+// conversions and two f16 products: 1134 instructions a chunk against 735 in the f16 form.)
 //
 // Numbers.  The other operand, one row of u or p, is float32, scaled by a power of two to just below 2^15 (u by its
 // largest, p has 1): its f16 value is column 0 of the product and, for float32 results, what that leaves is column
@@ -25,8 +24,9 @@ namespace {
 
 using namespace t8;
 
-constexpr int kWarps = 4;
-constexpr int kBlocksPerSm = 3;
+// Warps a block has, and blocks an SM: two chunks a warp, of 227 KB.
+constexpr int warps_of(int chunk_bytes) { return chunk_bytes == 16384 ? 6 : 4; }
+constexpr int blocks_of(int chunk_bytes) { return chunk_bytes == 16384 ? 1 : chunk_bytes == 8192 ? 3 : 4; }
 
 // Four consecutive elements, raw until they are used.
 __device__ __forceinline__ void widen4(float4 v, float *o) { o[0] = v.x; o[1] = v.y; o[2] = v.z; o[3] = v.w; }
@@ -49,20 +49,23 @@ __device__ __forceinline__ uint32_t rest_f16(float a, float b, uint32_t h)
 
 // PART: the one chunk that t_end ends inside; otherwise whole chunks.
 template <typename Tin, int D, int C, bool PART>
-__global__ void __launch_bounds__(32 * kWarps, kBlocksPerSm)
+__global__ void __launch_bounds__(32 * warps_of(C * D), blocks_of(C * D))
     landmarks8_kernel(const uint8_t *__restrict__ K8, const float *__restrict__ ks, const Tin *__restrict__ U,
                       Tin *__restrict__ L, float *__restrict__ beta, Cache8 p, float scale, int c0, int span, int t_end)
 {
-    constexpr int MT = C / 16, KS = D / 16, DT = D / 16, WORDS = D / 8, W = D / 32;
+    constexpr int MT = C / 16, KS = D / 16, W = warps_of(C * D);
     constexpr bool F32 = sizeof(Tin) == 4;
     constexpr float PTOP = 32768.0f;
     typedef typename Raw4<Tin>::type Raw;
+    extern __shared__ __align__(128) unsigned char s_chunks[];   // [warp][2][C][D]
     // the landmark query's columns 0, 1 (and 2: zeros, for all the others): [column][t][word: two values]
-    __shared__ __align__(16) uint32_t s_u[kWarps][3][4][2 * KS + 4];
+    __shared__ __align__(16) uint32_t s_u[W][3][4][2 * KS + 4];
+    __shared__ __align__(16) float s_out[W][D];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = lane >> 2, t = lane & 3;
-    const unsigned units = (unsigned)(p.B * p.Hkv) * (unsigned)span, step = gridDim.x * kWarps;
+    const unsigned units = (unsigned)(p.B * p.Hkv) * (unsigned)span, step = gridDim.x * W;
+    const uint32_t ring = sm100::smem_addr(s_chunks) + (uint32_t)warp * (2 * C * D);
 
-    unsigned unit = blockIdx.x * kWarps + warp;
+    unsigned unit = blockIdx.x * W + warp;
     if (unit >= units) return;   // whole warps leave; no block barrier follows
     if (r < 2 * KS / 4)   // columns without a value stay zero
 #pragma unroll
@@ -82,25 +85,24 @@ __global__ void __launch_bounds__(32 * kWarps, kBlocksPerSm)
         a.row0 = K8 + ((size_t)bg * p.T + (size_t)c * C) * D;
         return a;
     };
-    uint32_t buf[4][WORDS];
-    auto load_tile = [&](int n, const At &a) {
-        if (n < MT) load_k<D, PART>(buf[n & 3], a.row0 + 16 * n * D + 16 * t, r, a.rows - 1 - 16 * n);
-        else load_v<D, PART>(buf[n & 3], a.row0 + 16 * (n - MT) * D + (D / 8) * r, t, a.rows - 1 - 16 * (n - MT));
-    };
-    // the landmark query: lane (r, t) takes its word r of column block t (d = 64 (r / 4) + 16 t + 4 (r % 4))
-    const int ud = (64 * (r >> 2) + 16 * t + 4 * (r & 3)) % D;   // d = 64: lanes of r >= 4 repeat the others
+    auto load_chunk = [&](uint32_t slot, const At &a) { load_rows<D, C, PART>(ring + slot * (C * D), a.row0, a.rows - 1); };
+    // the landmark query: lane (r, t) takes d = 16 r + 4 t .. (d = 64: lanes of r >= 4 repeat the others)
+    const int ud = (16 * r + 4 * t) % D;
     auto load_u = [&](const At &a) { return *reinterpret_cast<const Raw *>(U + a.crow * D + ud); };
 
     At a = at(unit);
-#pragma unroll
-    for (int n = 0; n < 4; ++n) load_tile(n, a);
+    uint32_t slot = 0;
+    load_chunk(0, a);
+    cp_commit();
     Raw ur = load_u(a);
     float sc = __ldg(ks + a.crow);
     for (;;) {
         const bool more = units - unit > step;
-        const At an = at(more ? unit + step : unit);   // behind the last chunk its own tiles again: no branch around a load
+        const At an = at(more ? unit + step : unit);
+        if (more) load_chunk(slot ^ 1u, an);
+        cp_commit();
 
-        // the landmark query: lane (r, t) holds column r at d = 64 s + 16 t .. + 15
+        // the landmark query: lane (r, t) holds column r at d = 16 c + 4 t .. + 3
         uint32_t ub[KS][2];
         float fu;
         {
@@ -127,24 +129,25 @@ __global__ void __launch_bounds__(32 * kWarps, kBlocksPerSm)
             }
         }
 
-        // logits of rows r and r + 8 of each tile: columns 0 and 1 are lane t = 0's (the others' are zeros and stay unused)
+        cp_wait<1>();
+        __syncwarp();
+        const uint32_t tile0 = ring + slot * (C * D);
+
+        // logits of the keys that rows r of both halves of a tile stand for: columns 0 and 1 are lane t = 0's (the others'
+        // are zeros and stay unused)
         float x[MT][2];
 #pragma unroll
         for (int m = 0; m < MT; m += 2) {
             float d[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+            uint32_t w[2][KS][2];
+            read_keys<D>(tile0 + m * (16 * D), w[0]);
+            read_keys<D>(tile0 + (m + 1) * (16 * D), w[1]);
 #pragma unroll
-            for (int kk = 0; kk < KS; ++kk)
+            for (int c = 0; c < KS; ++c)
 #pragma unroll
-                for (int u = 0; u < 2; ++u) {
-                    const uint32_t w0 = buf[(m + u) & 3][kk], w1 = buf[(m + u) & 3][KS + kk];
-                    mma_f16(d[u], e4m3x2_to_f16x2(w0), e4m3x2_to_f16x2(w1), e4m3x2_to_f16x2(w0 >> 16),
-                            e4m3x2_to_f16x2(w1 >> 16), ub[kk][0], ub[kk][1]);
-                }
+                for (int u = 0; u < 2; ++u) mma_bytes(d[u], w[u][c][0], w[u][c][1], ub[c][0], ub[c][1]);
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
-                const int n = m + u + 4;
-                if (n < 2 * MT) load_tile(n, a);
-                else load_tile(n - 2 * MT, an);
                 x[m + u][0] = (d[u][0] + d[u][1]) * fu;
                 x[m + u][1] = (d[u][2] + d[u][3]) * fu;
             }
@@ -156,7 +159,7 @@ __global__ void __launch_bounds__(32 * kWarps, kBlocksPerSm)
         for (int m = 0; m < MT; ++m)
 #pragma unroll
             for (int h = 0; h < 2; ++h)
-                if (!PART || 16 * m + 8 * h + r < a.rows) mx = fmaxf(mx, x[m][h]);
+                if (!PART || 16 * m + key_row(r, h) < a.rows) mx = fmaxf(mx, x[m][h]);
 #pragma unroll
         for (int o = 4; o < 32; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, o));
 #pragma unroll
@@ -164,7 +167,7 @@ __global__ void __launch_bounds__(32 * kWarps, kBlocksPerSm)
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 const float d = x[m][h] - mx;
-                const float w = !PART || 16 * m + 8 * h + r < a.rows ? sm100::ex2_approx(d) : 0.f;
+                const float w = !PART || 16 * m + key_row(r, h) < a.rows ? sm100::ex2_approx(d) : 0.f;
                 z += w;
                 y = fmaf(w, fmaxf(d, -200.0f), y);   // w is 0 there
                 x[m][h] = w;
@@ -175,15 +178,15 @@ __global__ void __launch_bounds__(32 * kWarps, kBlocksPerSm)
             y += __shfl_xor_sync(0xFFFFFFFFu, y, o);
         }
 
-        // sum of p k: tile (w, hw) rows r / r + 8 are d = (D / 8) r + 4 w + 2 hw (+ 1)
-        float o[DT][4];
+        // sum of p k: tile c, rows r and r + 8 are d = 16 c + r (+ 8)
+        float o[KS][4];
 #pragma unroll
-        for (int i = 0; i < DT; ++i)
+        for (int i = 0; i < KS; ++i)
 #pragma unroll
             for (int e = 0; e < 4; ++e) o[i][e] = 0.f;
 #pragma unroll
         for (int m = 0; m < MT; ++m) {
-            // column r of p for keys 2t, 2t + 1 and 2t + 8, 2t + 9 of the tile
+            // column r of p for keys 4t, 4t + 1 and 4t + 2, 4t + 3 of the tile
             uint32_t b[2];
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
@@ -192,37 +195,34 @@ __global__ void __launch_bounds__(32 * kWarps, kBlocksPerSm)
                 if constexpr (F32) c = pack_f16(v, v - unpack_f16(c).x);
                 b[h] = movmatrix_t(t == 0 ? c : 0u);
             }
-            const uint32_t *v = buf[(MT + m) & 3];
 #pragma unroll
-            for (int w = 0; w < W; ++w) {
-#pragma unroll
-                for (int hw = 0; hw < 2; ++hw) {
-                    const uint32_t lo = __byte_perm(v[w], v[W + w], hw ? 0x7362 : 0x5140);
-                    const uint32_t hi = __byte_perm(v[2 * W + w], v[3 * W + w], hw ? 0x7362 : 0x5140);
-                    mma_f16(o[2 * w + hw], e4m3x2_to_f16x2(lo), e4m3x2_to_f16x2(lo >> 16), e4m3x2_to_f16x2(hi),
-                            e4m3x2_to_f16x2(hi >> 16), b[0], b[1]);
-                }
+            for (int c = 0; c < KS; c += 2) {
+                uint32_t w[2][2];
+                read_values<D>(tile0 + m * (16 * D), c, w);
+                mma_bytes(o[c], w[0][0], w[0][1], b[0], b[1]);
+                mma_bytes(o[c + 1], w[1][0], w[1][1], b[0], b[1]);
             }
-            const int n = MT + m + 4;
-            if (n < 2 * MT) load_tile(n, a);
-            else load_tile(n - 2 * MT, an);
-            if (m == 0) ur = load_u(an);
         }
+        ur = load_u(an);
         const float inv = 1.0f / z, g = inv * sc * (1.0f / PTOP);
         sc = __ldg(ks + an.crow);
         if (t == 0) {
-            float v[2 * DT];
 #pragma unroll
-            for (int i = 0; i < DT; ++i) {
-                v[2 * i] = (o[i][0] + o[i][1]) * g;
-                v[2 * i + 1] = (o[i][2] + o[i][3]) * g;
+            for (int c = 0; c < KS; ++c) {
+                s_out[warp][16 * c + r] = (o[c][0] + o[c][1]) * g;
+                s_out[warp][16 * c + r + 8] = (o[c][2] + o[c][3]) * g;
             }
-            store_n<2 * DT>(L + a.crow * D + (D / 8) * r, v);
+        }
+        __syncwarp();   // also: every lane has read the chunk, its buffer may be filled again
+        if (4 * lane < D) {
+            const float4 v = *reinterpret_cast<const float4 *>(&s_out[warp][4 * lane]);
+            store4(L + a.crow * D + 4 * lane, v);
         }
         if (beta && lane == 0) beta[a.crow] = logf(z) - y * inv * 0.6931471805599453f;
         if (!more) return;
         unit += step;
         a = an;
+        slot ^= 1u;
     }
 }
 
@@ -231,10 +231,12 @@ cudaError_t launch_t(const Cache8 &c, float scale, const uint8_t *K8, const floa
                      int c0, int c1, int t_end, cudaStream_t s)
 {
     auto run = [&](auto kern, int first, int span) {
-        const long long units = (long long)c.B * c.Hkv * span, blocks = (units + kWarps - 1) / kWarps;
-        const unsigned grid = (unsigned)(blocks < 148 * kBlocksPerSm ? blocks : 148 * kBlocksPerSm);
-        kern<<<grid, 32 * kWarps, 0, s>>>(K8, ks, static_cast<const Tin *>(U), static_cast<Tin *>(L), beta, c, scale, first,
-                                          span, t_end);
+        constexpr int W = warps_of(C * D), smem = W * 2 * C * D;
+        const long long units = (long long)c.B * c.Hkv * span, blocks = (units + W - 1) / W, most = 148 * blocks_of(C * D);
+        cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        if (e != cudaSuccess) return e;
+        kern<<<(unsigned)(blocks < most ? blocks : most), 32 * W, smem, s>>>(
+            K8, ks, static_cast<const Tin *>(U), static_cast<Tin *>(L), beta, c, scale, first, span, t_end);
         return cudaGetLastError();
     };
     const int whole = t_end / C;   // chunks before the one that t_end ends inside
