@@ -363,12 +363,12 @@ __global__ void __launch_bounds__(32 * kWarps, blocks_per_sm(D))
 }
 
 // How the rows are shared out: cs = 0: a warp a row (SOLO), else teams of cs blocks; and the time it is expected to
-// take, in the time of a warp's chunk (2.9 us with every SM full).  Weighed: a warp's turns of its row (the longest
+// take, in the time of a warp's chunk (1.9 us with every SM full).  Weighed: a warp's turns of its row (the longest
 // list and the mean), the start and end of a row (3 chunks for a lone warp, 1.5 for a team, its merge included), and how
-// often the resident warps start over.  8 rows of 65 slots go to teams of eight blocks (11.3 us; six 12.3, four 15.7),
-// 128 rows of 33 slots to teams of three (20.5 us; two 23.8, four, which queue, 31), 4072 rows of 33 slots to single
-// blocks (303 us; lone warps 347), 65536 rows of 17 slots and 2006 rows of 5 to lone warps (2.18 ms and 12.8 us; blocks
-// 2.54 ms and 20.1 us).
+// often the resident warps start over.  8 rows of 65 slots go to teams of eight blocks (8.5 us; six 8.8, four 10.6),
+// 128 rows of 33 slots to teams of three (17.1 us; two 17.9, four, which queue, 24), 4072 rows of 33 slots to single
+// blocks (188 us; lone warps 190, pairs 263), 65536 rows of 17 slots and 2006 rows of 5 to lone warps (1.35 ms and 11 us;
+// blocks 1.65 ms and 16 us).
 struct Share {
     int cs;
     double time;
@@ -438,13 +438,13 @@ static bool use_union(const Dims &p, hils_dtype in, hils_dtype out)
     if (force && strcmp(force, "union") == 0) return true;
     // The union's cost is known only for selections that have nothing to do with one another, its worst case: of V
     // visible chunks a block's BQ queries then want V (1 - (1 - k / V)^BQ).  A chunk of it takes 0.8 us and a
-    // block's set-up 5 us (8K prefill, 62 chunks on average: 835 us against 2.18 ms by rows; 509 queries at 130K, 810 chunks
-    // a block of which a query wants 33: 474 us against 303).
+    // block's set-up 5 us (8K prefill, 62 chunks on average: 835 us against 1.35 ms by rows; 509 queries at 130K, 810 chunks
+    // a block of which a query wants 33: 474 us against 189).
     const double BQ = 128 / p.G, V = (p.q_offset + 0.5 * p.N) / p.C + 1.0;
     const double U = V * (1.0 - pow(1.0 - fmin(1.0, p.k / V), BQ)) + BQ / p.C + 1.0;
     const double blocks = (double)p.B * p.Hkv * ((p.N + BQ - 1) / BQ) / 148.0;
     const double t_union = (blocks <= 1.0 ? 1.0 : blocks + 0.5) * (5.0 + 0.8 * fmin(U, V + 1.0));
-    return t_union < 2.9 * share_of(p, blocks_per_sm(p.d)).time;
+    return t_union < 1.9 * share_of(p, blocks_per_sm(p.d)).time;
 }
 
 cudaError_t launch_attend8(const Dims &p, hils_dtype in, hils_dtype out, const void *Q, const uint8_t *K8,
