@@ -19,7 +19,9 @@
 // Numbers.  A query row is scaled by a power of two to just below 2^15 and taken in f16: bf16 queries keep their 8 bits down
 // to 2^-29 of the row's largest, and below that an error of 2^-39 of it; float32 queries are two f16 pieces (22 bits).
 // P carries w_c vs_c / max_c'(w vs) and a factor 2^14 into f16 (2^-12 of the value down to 2^-28 of the row's
-// largest weight); for float32 results it is two f16 pieces.  All sums are float32.
+// largest weight); for float32 results it is two f16 pieces.  All sums are float32; the tensor cores cut what they add to an
+// accumulator off instead of rounding it, so for float32 results every product starts from zero and is added by the
+// float32 units (a chain of 264 products lost 1.6e-6 of the result, started afresh the error is 2e-7).
 //
 // A row's slots are split over the warps of one block or of a cluster of blocks, and the partial rows meet in shared
 // memory (distributed shared memory for a cluster): no workspace, no atomics, a fixed order.
@@ -57,7 +59,7 @@ __device__ __forceinline__ float ld_cluster(uint32_t addr, uint32_t rank)
 }
 
 // Blocks an SM holds: by registers, and for d = 128 by 16 KB of ring a warp.
-constexpr int blocks_per_sm(int D) { return D == 64 ? 4 : 3; }
+constexpr int blocks_per_sm(int D, int C, bool wide_out) { return (D == 64 ? 4 : 3) - (C == 128 && wide_out ? 1 : 0); }
 
 constexpr int ring_space(int D, int C)   // a warp's shared memory: its ring, later its partial rows
 {
@@ -67,7 +69,7 @@ constexpr int ring_space(int D, int C)   // a warp's shared memory: its ring, la
 
 // SOLO: every warp has a row of work to itself; otherwise the warps of a block, or of a cluster of cs blocks, share one.
 template <typename Tin, typename Tout, int D, int C, bool SOLO>
-__global__ void __launch_bounds__(32 * kWarps, blocks_per_sm(D))
+__global__ void __launch_bounds__(32 * kWarps, blocks_per_sm(D, C, sizeof(Tout) == 4))
     attend8_kernel(Dims p, int cs, int hgs, const Tin *__restrict__ Q, const uint8_t *__restrict__ K8,
                    const uint8_t *__restrict__ V8, const float *__restrict__ ks, const float *__restrict__ vs,
                    const int32_t *__restrict__ sel_idx, const float *__restrict__ sel_score, Tout *__restrict__ O)
@@ -230,8 +232,15 @@ __global__ void __launch_bounds__(32 * kWarps, blocks_per_sm(D))
                 for (int k = 0; k < KS; ++k)
 #pragma unroll
                     for (int u = 0; u < 2; ++u) {
-                        mma_bytes(sacc[m + u], w[u][k][0], w[u][k][1], qh[k][0], qh[k][1]);
-                        if constexpr (QHL) mma_bytes(sacc[m + u], w[u][k][0], w[u][k][1], ql[k][0], ql[k][1]);
+                        if constexpr (PHL) {
+                            float x[4] = {0.f, 0.f, 0.f, 0.f};
+                            if constexpr (QHL) mma_bytes(x, w[u][k][0], w[u][k][1], ql[k][0], ql[k][1]);
+                            mma_bytes(x, w[u][k][0], w[u][k][1], qh[k][0], qh[k][1]);
+                            add4(sacc[m + u], x);
+                        } else {
+                            mma_bytes(sacc[m + u], w[u][k][0], w[u][k][1], qh[k][0], qh[k][1]);
+                            if constexpr (QHL) mma_bytes(sacc[m + u], w[u][k][0], w[u][k][1], ql[k][0], ql[k][1]);
+                        }
                     }
             });
 
@@ -298,8 +307,14 @@ __global__ void __launch_bounds__(32 * kWarps, blocks_per_sm(D))
                         read_values<D>(tile + u * 16 * D, k, w);
 #pragma unroll
                         for (int v = 0; v < 2; ++v) {
-                            mma_bytes(oacc[k + v], w[v][0], w[v][1], b0, b1);
-                            if constexpr (PHL) mma_bytes(oacc[k + v], w[v][0], w[v][1], r0, r1);
+                            if constexpr (PHL) {
+                                float x[4] = {0.f, 0.f, 0.f, 0.f};
+                                mma_bytes(x, w[v][0], w[v][1], r0, r1);
+                                mma_bytes(x, w[v][0], w[v][1], b0, b1);
+                                add4(oacc[k + v], x);
+                            } else {
+                                mma_bytes(oacc[k + v], w[v][0], w[v][1], b0, b1);
+                            }
                         }
                     }
                 }
@@ -394,7 +409,7 @@ cudaError_t launch_t(const Dims &p, const void *Q, const uint8_t *K8, const uint
                      const int32_t *sel_idx, const float *sel_score, void *O, cudaStream_t s)
 {
     const int hgs = (p.G + kHeads - 1) / kHeads;
-    const int cs = share_of(p, blocks_per_sm(D)).cs;
+    const int cs = share_of(p, blocks_per_sm(D, C, sizeof(Tout) == 4)).cs;
     const long long units = (long long)p.N * hgs;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(cs ? units * cs : (units + kWarps - 1) / kWarps), (unsigned)(p.B * p.Hkv));
@@ -444,7 +459,7 @@ static bool use_union(const Dims &p, hils_dtype in, hils_dtype out)
     const double U = V * (1.0 - pow(1.0 - fmin(1.0, p.k / V), BQ)) + BQ / p.C + 1.0;
     const double blocks = (double)p.B * p.Hkv * ((p.N + BQ - 1) / BQ) / 148.0;
     const double t_union = (blocks <= 1.0 ? 1.0 : blocks + 0.5) * (5.0 + 0.8 * fmin(U, V + 1.0));
-    return t_union < 1.9 * share_of(p, blocks_per_sm(p.d)).time;
+    return t_union < 1.9 * share_of(p, blocks_per_sm(p.d, p.C, false)).time;
 }
 
 cudaError_t launch_attend8(const Dims &p, hils_dtype in, hils_dtype out, const void *Q, const uint8_t *K8,

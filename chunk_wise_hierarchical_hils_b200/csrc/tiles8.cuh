@@ -98,6 +98,12 @@ __device__ __forceinline__ void mma_bytes(float (&d)[4], uint32_t w0, uint32_t w
     mma_f16(d, e4m3x2_to_f16x2(w0), e4m3x2_to_f16x2(w1), e4m3x2_to_f16x2(w0 >> 16), e4m3x2_to_f16x2(w1 >> 16), b0, b1);
 }
 
+__device__ __forceinline__ void add4(float (&a)[4], const float (&x)[4])
+{
+#pragma unroll
+    for (int e = 0; e < 4; ++e) a[e] += x[e];
+}
+
 // 8 x 8 matrix of 16-bit elements, transposed across the warp
 __device__ __forceinline__ uint32_t movmatrix_t(uint32_t x)
 {
