@@ -297,6 +297,147 @@ def test_attend(shape, dtype, out):
     print("worst error / bound %.3g" % compare(p, h, O, out))
 
 
+UNION_SHAPES = [
+    (1, 4, 1, 2, 2, 128, 64, 1, 0),                 # two queries, one chunk
+    (1, 4, 1, 33, 500, 128, 64, 3, 190),            # a second block of one query
+    (1, 1, 1, 129, 300, 128, 64, 2, 100),           # one head: 128 queries a block
+    (1, 2, 1, 200, 4000, 128, 64, 20, 3700),        # many chunks, few of them shared
+    (2, 16, 2, 50, 700, 128, 64, 9, 600),           # eight heads a group
+    (1, 16, 1, 40, 900, 128, 64, 5, 800),           # sixteen
+    (1, 4, 1, 64, 64, 128, 64, 0, 0),               # own chunk only, a lone last pair
+    (1, 4, 1, 128, 40000, 128, 64, 37, 39000),      # the longest list of slots that the kernel's shared memory holds, nearly
+]
+
+
+@pytest.mark.parametrize("kernel", ["rows", "union"])
+@pytest.mark.parametrize("shape", [s for s in SHAPES if s[3] > 1 and s[5:7] == (128, 64) and s[1] // s[2] in (1, 2, 4, 8, 16)]
+                         + UNION_SHAPES, ids=lambda s: "x".join(map(str, s)))
+def test_attend_kernels(shape, kernel, monkeypatch):
+    """Both kernels of bf16 prefill, whatever the choice between them."""
+    monkeypatch.setenv("HILS_Q8_KERNEL", kernel)
+    p, h, dev = attend_case(*shape, "bf16", "bf16", 500 + sum(shape))
+    O = attend(p, dev)
+    O2 = attend(p, dev)
+    ok()
+    assert torch.equal(O.view(torch.int16), O2.view(torch.int16))
+    compare(p, h, O, "bf16")
+
+
+def test_attend_union_on_shared_selections(monkeypatch):
+    """Neighbouring queries that keep the same chunks (the union is short) and rows with nothing selected."""
+    monkeypatch.setenv("HILS_Q8_KERNEL", "union")
+
+    def edit(h, r):
+        h["sel"][:] = h["sel"][:, :, :1]                   # the first query's chunks for all
+        h["sel"][:, :, 5:9] = -1
+    p, h, dev = attend_case(1, 8, 2, 100, 2000, 128, 64, 16, 1880, "bf16", "bf16", 520, edit=edit)
+    O = attend(p, dev)
+    ok()
+    compare(p, h, O, "bf16")
+
+
+@pytest.mark.parametrize("kernel", ["rows", "union"])
+def test_attend_wide_scales_kernels(kernel, monkeypatch):
+    monkeypatch.setenv("HILS_Q8_KERNEL", kernel)
+    p, h, dev = attend_case(1, 8, 2, 140, 400, 128, 64, 5, 200, "bf16", "bf16", 530, spread=60.0)
+    O = attend(p, dev)
+    ok()
+    compare(p, h, O, "bf16")
+
+
+def test_attend_zero_queries_and_zero_scales():
+    """Queries of zeros see every key alike; chunks of scale zero (keys or values) are chunks of zeros."""
+    def edit(h, r):
+        h["ks"][:, :, ::2] = np.where(np.isnan(h["ks"][:, :, ::2]), np.nan, 0.0)
+        h["vs"][:, :, 1::3] = np.where(np.isnan(h["vs"][:, :, 1::3]), np.nan, 0.0)
+    for N, q0 in ((1, 700), (96, 600)):
+        p, h, dev = attend_case(1, 8, 2, N, 800, 128, 64, 6, q0, "bf16", "bf16", 540 + N, edit=edit)
+        h["Q"][:, 1::2] = 0.0
+        dev["Q"][:, 1::2] = 0
+        O = attend(p, dev)
+        ok()
+        compare(p, h, O, "bf16")
+
+
+@pytest.mark.parametrize("shape,dtype,rows", [
+    ((1, 2, 2, 1003, 1024, 64, 32, 4, 0), "f32", range(0, 1003, 41)),        # rows enough for a warp each
+    ((4, 32, 8, 3, 2000, 128, 64, 12, 1990), "bf16", None),                   # teams of one block
+    ((2, 8, 2, 5, 3000, 64, 64, 40, 2900), "f32", None),                      # teams of several
+], ids=["lone", "block", "cluster"])
+def test_attend_shares_of_rows(shape, dtype, rows):
+    p, h, dev = attend_case(*shape, dtype, dtype, 550 + sum(shape))
+    O = attend(p, dev)
+    ok()
+    compare(p, h, O, dtype, rows=rows)
+
+
+def test_a_cache_beyond_four_gigabytes():
+    """Offsets past 32 bits: the last tokens of a 4M-token cache of eight kv-heads (4.3 GB a side)."""
+    B, H, Hkv, T, d, C, slots = 1, 16, 8, 1 << 22, 128, 64, 5
+    r = np.random.default_rng(560)
+    nL = T // C
+    K8 = torch.zeros((B, Hkv, T, d), dtype=torch.uint8, device=DEV)
+    V8 = torch.zeros_like(K8)
+    ks, vs = torch.zeros((B, Hkv, nL), device=DEV), torch.zeros((B, Hkv, nL), device=DEV)
+    t0 = T - 5 * C - 17
+    x64, x = zip(*(rng_rows(r, (B, Hkv, T - t0, d), "bf16") for _ in range(2)))
+    p = hils.problem(B, H, Hkv, 1, T, d, C, slots, T - 1, hils.HILS_BF16, hils.HILS_BF16)
+    hils.hils_cache_append_q8(p, x[0][:, :, :17].contiguous(), x[1][:, :, :17].contiguous(), K8, V8, ks, vs, t0, t0 + 17)
+    hils.hils_cache_append_q8(p, x[0][:, :, 17:].contiguous(), x[1][:, :, 17:].contiguous(), K8, V8, ks, vs, t0 + 17, T)
+    back = [torch.empty_like(x[0]) for _ in range(2)]
+    hils.hils_cache_read_q8(p, K8, V8, ks, vs, back[0], back[1], t0, T)
+    U64, U = rng_rows(r, (B, Hkv, nL, d), "bf16")
+    L = torch.zeros((B, Hkv, nL, d), dtype=torch.bfloat16, device=DEV)
+    hils.hils_landmarks_q8(p, K8, ks, U, L, None, nL - 5, nL)
+    ok()
+    assert not K8[:, :, :t0].any() and not V8[:, :, :t0].any()
+    # the last kv-heads' tails on the host
+    tail = 6 * C
+    base = T - tail
+    for g in (0, Hkv - 1):
+        data, scale = np.zeros((tail, d), np.uint8), np.zeros(6, np.float32)
+        ref.append(x64[0][0, g, :17], data, scale, t0 - base, C)
+        ref.append(x64[0][0, g, 17:], data, scale, t0 + 17 - base, C)
+        assert np.array_equal(K8[0, g, base:].cpu().numpy(), data)
+        assert np.array_equal(ks[0, g, -6:].cpu().numpy(), scale)
+        val = ref.TABLE[data] * scale.astype(np.float64)[np.arange(tail) // C, None]
+        got = back[0][0, g].double().cpu().numpy()
+        assert np.array_equal(got, val[t0 - base:])
+        for c in (1, 5):
+            k, u = val[c * C:(c + 1) * C], U64[0, g, nL - 6 + c]
+            want, _ = ref.landmarks(k, u, 1.0 / math.sqrt(d))
+            e = 2 * (d + 8) * 2.0 ** -24 * np.max(np.abs(k) @ np.abs(u)) / math.sqrt(d) + (C + 40) * 2.0 ** -24
+            tol = e * np.max(np.abs(k)) + ref.half_step("bf16") * np.abs(want)
+            assert np.all(np.abs(L[0, g, nL - 6 + c].double().cpu().numpy() - want) <= tol)
+    # a query that keeps the five chunks before its own
+    Q64, Q = rng_rows(r, (B, H, 1, d), "bf16")
+    sel = torch.arange(nL - 6, nL - 1, dtype=torch.int32, device=DEV).view(1, 1, 1, slots).expand(B, Hkv, 1, slots).contiguous()
+    score = torch.zeros((B, H, 1, slots + 1), device=DEV)
+    O = attend(p, dict(Q=Q, K8=K8, V8=V8, ks=ks, vs=vs, sel=sel, score=score))
+    ok()
+    h = dict(Q=Q64, K8=K8[:, :, base:].cpu().numpy(), V8=V8[:, :, base:].cpu().numpy(), ks=ks[:, :, -6:].cpu().numpy(),
+             vs=vs[:, :, -6:].cpu().numpy(), sel=sel.cpu().numpy() - (nL - 6), score=score.cpu().numpy())
+    pt = hils.problem(B, H, Hkv, 1, tail, d, C, slots, tail - 1, hils.HILS_BF16, hils.HILS_BF16)
+    compare(pt, h, O, "bf16")
+
+
+def test_a_stalled_prefill_reports_a_timeout(monkeypatch):
+    """The bounded waits of the tensor-core kernel: a wait that nothing ends expires, the status tells, the next call is right."""
+    monkeypatch.setenv("HILS_Q8_KERNEL", "union")
+    p, h, dev = attend_case(1, 8, 2, 200, 600, 128, 64, 4, 400, "bf16", "bf16", 570)
+    try:
+        hils.hils_set_wait_limit(2_000_000)                 # 2 ms
+        hils.hils_debug_inject_stall(1)
+        attend(p, dev)
+        assert hils.hils_sync_status() == hils.HILS_ERR_TIMEOUT
+    finally:
+        hils.hils_debug_inject_stall(0)
+        hils.hils_set_wait_limit(0)
+    O = attend(p, dev)
+    ok()
+    compare(p, h, O, "bf16", rows=range(0, 200, 7))
+
+
 @pytest.mark.parametrize("shape", [(1, 4, 1, 1, 1000, 128, 64, 9, 999), (1, 8, 2, 140, 400, 128, 64, 5, 200),
                                    (1, 4, 2, 30, 300, 64, 32, 5, 200)], ids=lambda s: "x".join(map(str, s)))
 @pytest.mark.parametrize("dtype,out", [("bf16", "bf16"), ("f32", "f32")])
