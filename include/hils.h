@@ -345,7 +345,16 @@ HILS_API hils_status hils_landmarks_q8(const hils_problem *p, const void *K8, co
  * may be any finite floats that are not negative.  The result is defined when the bytes the call's
  * queries may see (t < q_offset + N, in selected chunks) hold no NaN and the
  * products stay in float range; bytes behind them may be anything.
- * Precision: products accumulate in float32.
+ * Precision: products accumulate in float32.  For float32 results queries and
+ * probabilities enter them with 22 bits.  For bf16 results the probabilities
+ * are rounded to f16 (2^-12 of a weight, down to 2^-28 of the row's largest),
+ * and prefill on the tensor cores takes a bf16 query exactly but for elements
+ * below 2^-10 of its largest, which lose up to 2^-18 of that.  Keys and values
+ * enter exactly.
+ * Kernel choice: rows of queries one by one (every shape), or for bf16 prefill
+ * with d = 128 and C = 64 the union of a query block's chunks on the tensor
+ * cores where that is expected to take less time.  HILS_Q8_KERNEL=rows or
+ * =union forces one (the latter where it covers the shape; a test control).
  */
 HILS_API hils_status hils_chunk_attend_fuse_q8_workspace_size(const hils_problem *p, size_t *bytes);
 HILS_API hils_status hils_chunk_attend_fuse_q8(const hils_problem *p, const void *Q, const void *K8, const void *V8,
