@@ -111,7 +111,12 @@ __global__ void __launch_bounds__(32 * kWarps, blocks_per_sm(D, C, sizeof(Tout) 
 
     // The own chunk, whose rows behind the query are not seen, is the first in the order of work and past chunks (whole
     // ones) follow: turn 0 is slot k, turn x > 0 slot x - 1.  This warp's turns are me, me + nw, ..
-    auto chunk_of = [&](int j) { return j < p.k ? __ldg(si + j) : j == p.k ? ci : -1; };
+    // An entry that is no past chunk of the query is an empty slot: nothing outside the cache is read for it.
+    auto chunk_of = [&](int j) {
+        if (j >= p.k) return j == p.k ? ci : -1;
+        const int x = __ldg(si + j);
+        return (unsigned)x < (unsigned)ci ? x : -1;
+    };
     int turn = me, c = turn == 0 ? ci : chunk_of(turn <= p.k ? turn - 1 : ns);
     while (c < 0 && turn + nw < ns) { turn += nw; c = chunk_of(turn - 1); }
     const int own_top = (int)(pos - (long long)ci * C);

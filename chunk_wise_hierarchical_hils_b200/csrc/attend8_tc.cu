@@ -192,7 +192,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int i = tid; i < nwords; i += kThreads) bitmap[i] = 0u;
     const int32_t *sel_base = sel_idx + (bg * p.N + q0) * p.k;
 #pragma unroll 4
-    for (int e = tid; e < nq * p.k; e += kThreads) selbuf[e] = __ldg(sel_base + e);
+    for (int e = tid; e < nq * p.k; e += kThreads) {
+        // an entry that is no past chunk of its query is an empty slot: nothing outside the cache is read for it
+        const int c = __ldg(sel_base + e), own_c = (int)(((long long)p.q_offset + q0 + e / p.k) / kChunk);
+        selbuf[e] = (unsigned)c < (unsigned)own_c ? c : -1;
+    }
 #pragma unroll 4
     for (int e = tid; e < G * nq * ns; e += kThreads) {
         const int h = e / (nq * ns), rem = e - h * (nq * ns), qi = rem / ns;
@@ -267,7 +271,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) *n_union_p = running;
     }
     // each query's chunks in ascending order with the slot each came from: one thread per (query, slot) counts the
-    // query's smaller chunks (chunks are distinct)
+    // query's smaller chunks (chunks are distinct; of one named twice, against the rule, the first slot counts)
     for (int e = tid - 32; e >= 0 && e < nq * ns; e += kThreads - 32) {
         const int qi = e / ns, j = e % ns;
         const int own_c = (int)(((long long)p.q_offset + q0 + qi) / kChunk);
@@ -276,7 +280,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         qvs[qi * ns + j] = c < 0 ? 0.f : __ldg(vsb + c);
         if (c < 0) continue;
         int rank = 0;
-        for (int j2 = 0; j2 < p.k; ++j2) rank += (unsigned)sl[j2] < (unsigned)c;   // -1 never counts
+        for (int j2 = 0; j2 < p.k; ++j2)   // -1 never counts
+            rank += (unsigned)sl[j2] < (unsigned)c + (unsigned)(j2 < j);
         rank += own_c < c;
         qlist[qi * ns + rank] = c;
         qslot[qi * ns + rank] = j;

@@ -340,11 +340,14 @@ HILS_API hils_status hils_landmarks_q8(const hils_problem *p, const void *K8, co
 /*
  * hils_chunk_attend_fuse over the 8-bit cache, with the same selection
  * arguments (also those of hils_score_select_window, on its k'), ownership and
- * errors.  A slot with sel_idx -1 is empty whatever its score, and a slot with
- * score -INFINITY has no weight; a row without any weight is zero.  The scales
- * may be any finite floats that are not negative.  The result is defined when the bytes the call's
- * queries may see (t < q_offset + N, in selected chunks) hold no NaN and the
- * products stay in float range; bytes behind them may be anything.
+ * errors.  A slot with sel_idx -1 (or any value that is no past chunk of its
+ * query) is empty whatever its score, and a slot with score -INFINITY has no
+ * weight; a row without any weight is zero.  A row must not name a chunk twice:
+ * what its slots count together is then unspecified.
+ * The scales may be any finite floats that are not negative.  The result is
+ * defined when the bytes the call's queries may see (t < q_offset + N, in
+ * selected chunks) hold no NaN and the products stay in float range; bytes
+ * behind them may be anything.
  * Precision: products accumulate in float32.  For float32 results queries and
  * probabilities enter them with 22 bits.  For bf16 results the probabilities
  * are rounded to f16 (2^-12 of a weight, down to 2^-28 of the row's largest),

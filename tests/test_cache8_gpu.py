@@ -485,6 +485,41 @@ def test_attend_empty_slots_and_masked_scores(N, dtype, out):
     compare(p, h, O, out)
 
 
+@pytest.mark.parametrize("N,kernel", [(1, "rows"), (40, "rows"), (140, "rows"), (140, "union")])
+def test_attend_entries_outside_the_past(N, kernel, monkeypatch):
+    """Entries that name no past chunk (the own one, later ones, far outside, negative) are empty slots."""
+    monkeypatch.setenv("HILS_Q8_KERNEL", kernel)
+
+    def edit(h, r):
+        own = (450 + np.arange(N)) // 64
+        bad = np.stack([own, own + 1, np.full(N, 2 ** 31 - 1), np.full(N, -2 ** 31), np.full(N, 10 ** 6), np.full(N, -2)], -1)
+        h["given"] = h["sel"].copy()
+        at = r.integers(0, 6, (h["sel"].shape[1], N))
+        for g in range(h["sel"].shape[1]):
+            h["given"][0, g, :, 2] = bad[np.arange(N), at[g]]
+        h["sel"][:, :, :, 2] = -1
+        h["score"][:, :, :, 2] = 1.0
+    p, h, dev = attend_case(1, 8, 2, N, 600, 128, 64, 5, 450, "bf16", "bf16", 385 + N, edit=edit)
+    dev["sel"] = torch.from_numpy(h["given"]).to(DEV)
+    O = attend(p, dev)
+    ok()
+    compare(p, h, O, "bf16")
+
+
+@pytest.mark.parametrize("kernel", ["rows", "union"])
+def test_attend_a_chunk_named_twice_harms_no_other_row(kernel, monkeypatch):
+    monkeypatch.setenv("HILS_Q8_KERNEL", kernel)
+    N = 140
+
+    def edit(h, r):
+        h["sel"][:, :, ::2, 3] = h["sel"][:, :, ::2, 0]
+        h["sel"][:, :, ::6] = h["sel"][:, :, ::6, :1]       # in every slot
+    p, h, dev = attend_case(1, 8, 2, N, 600, 128, 64, 5, 450, "bf16", "bf16", 527, edit=edit)
+    O = attend(p, dev)
+    ok()
+    compare(p, h, O, "bf16", rows=range(1, N, 2))
+
+
 @pytest.mark.parametrize("N", [1, 64])
 def test_attend_extreme_scores(N):
     """Scores at the type's lowest and highest values."""
