@@ -59,7 +59,8 @@ constexpr uint32_t kQTile = kRows * kD;              // bytes of one of the quer
 constexpr uint32_t kPair8 = 2 * kChunk * kD;         // a pair of e4m3 tiles
 constexpr uint32_t kPair16 = 2 * kPair8;             // f16 values: [c0 d0-63 | c1 d0-63 | c0 d64-127 | c1 d64-127]
 constexpr unsigned long long kDrainNs = 2000000000ull;
-constexpr int kPolyPairEvery = 4;
+constexpr int kPolyPairEvery = 0;   // every exponential on the special-function unit (8K prompt: 810 us; one pair in eight by
+                                      // polynomial 823, in four 833, in two 940)
 constexpr float kTopW = 16384.0f;
 
 constexpr uint32_t IDESC_QK2 = idesc_f16_f32(128, 128, false, false);   // kind::f8f6f4 reads the same fields: 0 is e4m3
