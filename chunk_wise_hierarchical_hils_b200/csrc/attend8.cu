@@ -189,6 +189,7 @@ __global__ void __launch_bounds__(32 * kWarps, blocks_per_sm(D, C, sizeof(Tout) 
             top = fmaxf(top, fabsf(s[u]));
         }
         top = warp_max(top);
+        if (top > 0.f) top = fmaxf(top, 1e-34f);   // its inverse stays finite
         const float f = top > 0.f ? 16384.0f / top : 1.0f;
 #pragma unroll
         for (int u = 0; u < 3; ++u)

@@ -452,6 +452,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         top = fmaxf(top, x[u]);
                     }
                 top = max8(top);
+                if (top > 0.f) top = fmaxf(top, 1e-34f);   // its inverse stays finite
                 const float f = top > 0.f ? kTopW / top : 1.0f;
 #pragma unroll
                 for (int u = 0; u < S8; ++u)

@@ -337,6 +337,20 @@ def test_attend_union_on_shared_selections(monkeypatch):
 
 
 @pytest.mark.parametrize("kernel", ["rows", "union"])
+def test_attend_smallest_and_largest_scales(kernel, monkeypatch):
+    """Value scales down to float32's subnormals and up to 2^119, in different kv-heads."""
+    monkeypatch.setenv("HILS_Q8_KERNEL", kernel)
+
+    def edit(h, r):
+        for g, v in enumerate((1e-40, 2.0 ** -100, 2.0 ** 119)):
+            h["vs"][:, g] = np.where(np.isnan(h["vs"][:, g]), np.nan, np.float32(v))
+    p, h, dev = attend_case(1, 12, 3, 100, 400, 128, 64, 5, 250, "bf16", "bf16", 535, edit=edit)
+    O = attend(p, dev)
+    ok()
+    compare(p, h, O, "bf16")
+
+
+@pytest.mark.parametrize("kernel", ["rows", "union"])
 def test_attend_wide_scales_kernels(kernel, monkeypatch):
     monkeypatch.setenv("HILS_Q8_KERNEL", kernel)
     p, h, dev = attend_case(1, 8, 2, 140, 400, 128, 64, 5, 200, "bf16", "bf16", 530, spread=60.0)
