@@ -159,42 +159,51 @@ __global__ void __launch_bounds__(32 * kWarps, blocks_per_sm(D, C, sizeof(Tout) 
     // this lane's columns of the products are heads 2t and 2t + 1
     const float fq0 = __shfl_sync(0xFFFFFFFFu, fq, 8 * t), fq1 = __shfl_sync(0xFFFFFFFFu, fq, 8 * t + 4);
 
-    // slot factors w_c vs_c over the row's largest, times 2^14; a slot without a chunk has no weight, whatever its score
-    for (int h = SOLO ? 0 : warp; h < kHeads; h += SOLO ? 1 : kWarps) {
-        if (h >= nh) {   // columns without a head: no weight
-            for (int jj = lane; jj < ns; jj += 32) s_w[h][jj] = 0.f;
-            continue;
-        }
-        float s[3], v[3], mx = -INFINITY, z = 0.f, top = 0.f;
+    // slot factors w_c vs_c over the row's largest, times 2^14; a slot without a chunk has no weight, whatever its score.
+    // The loads of all of a warp's heads are in flight together.
+    {
+        constexpr int HW = SOLO ? kHeads : kHeads / kWarps;   // heads a warp works out
+        float s[HW][3], v[3];
 #pragma unroll
         for (int u = 0; u < 3; ++u) {
-            const int jj = lane + 32 * u;
-            const int cc = chunk_of(jj);
-            s[u] = cc >= 0 ? __ldg(sel_score + ((bg * p.G + h0 + h) * p.N + i) * ns + jj) : -INFINITY;
+            const int jj = lane + 32 * u, cc = chunk_of(jj);
             v[u] = cc >= 0 ? __ldg(vs + bg * p.nL + cc) : 0.f;
-            if (h == 0 && jj < ns) s_chunk[jj] = cc;
-            mx = fmaxf(mx, s[u]);
-        }
-        mx = warp_max(mx);
+            if ((SOLO || warp == 0) && jj < ns) s_chunk[jj] = cc;
 #pragma unroll
-        for (int u = 0; u < 3; ++u) {
-            s[u] = (s[u] == -INFINITY) ? 0.f : expf(s[u] - mx);
-            z += s[u];
+            for (int q = 0; q < HW; ++q) {
+                const int h = SOLO ? q : warp + q * kWarps;
+                s[q][u] = cc >= 0 && h < nh ? __ldg(sel_score + ((bg * p.G + h0 + h) * p.N + i) * ns + jj) : -INFINITY;
+            }
         }
-        z = warp_sum(z);
-        const float iz = z == 0.f ? 0.f : 1.0f / z;
 #pragma unroll
-        for (int u = 0; u < 3; ++u) {
-            s[u] = s[u] == 0.f ? 0.f : s[u] * iz * v[u];
-            top = fmaxf(top, fabsf(s[u]));
+        for (int q = 0; q < HW; ++q) {
+            const int h = SOLO ? q : warp + q * kWarps;
+            if (h >= nh) {   // columns without a head: no weight
+                for (int jj = lane; jj < ns; jj += 32) s_w[h][jj] = 0.f;
+                continue;
+            }
+            const float mx = warp_max(fmaxf(fmaxf(s[q][0], s[q][1]), s[q][2]));
+            float z = 0.f, top = 0.f;
+#pragma unroll
+            for (int u = 0; u < 3; ++u) {
+                s[q][u] = (s[q][u] == -INFINITY) ? 0.f : expf(s[q][u] - mx);
+                z += s[q][u];
+            }
+            z = warp_sum(z);
+            const float iz = z == 0.f ? 0.f : 1.0f / z;
+#pragma unroll
+            for (int u = 0; u < 3; ++u) {
+                s[q][u] = s[q][u] == 0.f ? 0.f : s[q][u] * iz * v[u];
+                top = fmaxf(top, s[q][u]);
+            }
+            top = warp_max(top);
+            if (top > 0.f) top = fmaxf(top, 1e-34f);   // its inverse stays finite
+            const float f = top > 0.f ? 16384.0f / top : 1.0f;
+#pragma unroll
+            for (int u = 0; u < 3; ++u)
+                if (lane + 32 * u < ns) s_w[h][lane + 32 * u] = s[q][u] * f;
+            if (lane == 0) s_top[h] = top > 0.f ? top * (1.0f / 16384.0f) : 0.f;
         }
-        top = warp_max(top);
-        if (top > 0.f) top = fmaxf(top, 1e-34f);   // its inverse stays finite
-        const float f = top > 0.f ? 16384.0f / top : 1.0f;
-#pragma unroll
-        for (int u = 0; u < 3; ++u)
-            if (lane + 32 * u < ns) s_w[h][lane + 32 * u] = s[u] * f;
-        if (lane == 0) s_top[h] = top > 0.f ? top * (1.0f / 16384.0f) : 0.f;
     }
     if constexpr (SOLO) __syncwarp();
     else __syncthreads();
