@@ -407,7 +407,8 @@ struct Share {
 Share share_of(const Dims &p, int per_sm)
 {
     const double rows = (double)p.B * p.Hkv * ((p.G + kHeads - 1) / kHeads) * p.N, blocks = 148.0 * per_sm;
-    const int ns = p.k + 1;
+    // slots that can hold a chunk: no more than the last query has chunks before its own
+    const int ns = (int)fmin(p.k, ((double)p.q_offset + p.N - 1) / p.C) + 1;
     auto rounds = [](double x) { return x <= 1.0 ? 1.0 : x <= 4.0 ? ceil(x) + 0.25 : x + 0.5; };
     Share best = {0, rounds(rows / (blocks * kWarps)) * (ns + 3.0)};
     for (int cs = 1; cs <= 8; ++cs) {
