@@ -11,7 +11,8 @@
 //   S^T = K Q^T     A = 16 keys x 16 of d, B = 8 heads
 //   O^T = V^T P^T   A = 16 of d x 16 keys (bytes transposed as they are read); P^T comes from S^T's accumulators by
 //                   movmatrix
-// e4m3 becomes f16 (exact) in registers.  The eight columns are heads: a group of more than eight is two rows of work.  A
+// e4m3 becomes f16 (exact) in registers.  The eight columns are heads (float32 queries or results: four heads and their
+// second pieces); a group of more is two or more rows of work.  A
 // chunk is a stream of pairs of tiles, its keys' and then its values', through a ring of up to four pairs: once a pair is
 // used its place is filled with the pair four further on, which runs on into the warp's next chunk, so a warp has
 // 8 to 16 KB in flight or in use.
@@ -41,7 +42,9 @@ namespace {
 using namespace t8;
 
 constexpr int kWarps = 4;
-constexpr int kHeads = 8;      // heads a row of work covers
+constexpr int kCols = 8;       // columns of a product
+// Heads a row of work covers: one a column; with float32 queries or results four, whose second pieces take the others.
+constexpr int heads_of(bool wide) { return wide ? 4 : 8; }
 constexpr int kMaxSlots = HILS_MAX_K + 1;
 
 __device__ __forceinline__ uint32_t cluster_rank() { uint32_t r; asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r)); return r; }
@@ -63,7 +66,7 @@ constexpr int blocks_per_sm(int D, int C, bool wide_out) { return (D == 64 ? 4 :
 
 constexpr int ring_space(int D, int C)   // a warp's shared memory: its ring, later its partial rows
 {
-    const int ring = (C / 16 < 4 ? C / 16 : 4) * 32 * D, rows = (kHeads * (D + 4) * 4 + 127) / 128 * 128;
+    const int ring = (C / 16 < 4 ? C / 16 : 4) * 32 * D, rows = (kCols * (D + 4) * 4 + 127) / 128 * 128;
     return ring > rows ? ring : rows;
 }
 
@@ -75,26 +78,27 @@ __global__ void __launch_bounds__(32 * kWarps, blocks_per_sm(D, C, sizeof(Tout) 
                    const int32_t *__restrict__ sel_idx, const float *__restrict__ sel_score, Tout *__restrict__ O)
 {
     constexpr bool QHL = sizeof(Tin) == 4, PHL = sizeof(Tout) == 4;
-    constexpr int MT = C / 16, KS = D / 16;
+    constexpr bool WIDE = QHL || PHL;                 // columns 4 .. 7: the second pieces of columns 0 .. 3
+    constexpr int HEADS = heads_of(WIDE), MT = C / 16, KS = D / 16;
     constexpr int NP = MT, RP = NP < 4 ? NP : 4;      // pairs of tiles a chunk is (half of them keys), pairs in a ring
     constexpr int PAIR = 32 * D;
     constexpr int ROWS = SOLO ? kWarps : 1;           // rows of work a block has
     constexpr int PITCH = D + 4;                      // of a row of partial results: lanes of a fragment on distinct banks
     constexpr int SPACE = ring_space(D, C);
     extern __shared__ __align__(128) unsigned char s_ring[];   // [warp][SPACE]: its ring, then its partial rows
-    __shared__ float s_weights[ROWS][kHeads][kMaxSlots];
-    __shared__ float s_tops[ROWS][kHeads];
+    __shared__ float s_weights[ROWS][HEADS][kMaxSlots];
+    __shared__ float s_tops[ROWS][HEADS];
     __shared__ int s_chunks[ROWS][kMaxSlots];
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, r = lane >> 2, t = lane & 3;
     const int rank = !SOLO && cs > 1 ? (int)cluster_rank() : 0;
     const int unit = SOLO ? blockIdx.x * kWarps + warp : blockIdx.x / cs, i = unit / hgs;
     if (SOLO && i >= p.N) return;                     // whole warps leave; a block of lone warps has no barrier
-    float (&s_w)[kHeads][kMaxSlots] = s_weights[SOLO ? warp : 0];
-    float (&s_top)[kHeads] = s_tops[SOLO ? warp : 0];
+    float (&s_w)[HEADS][kMaxSlots] = s_weights[SOLO ? warp : 0];
+    float (&s_top)[HEADS] = s_tops[SOLO ? warp : 0];
     int (&s_chunk)[kMaxSlots] = s_chunks[SOLO ? warp : 0];
     const size_t bg = blockIdx.y;
-    const int h0 = (unit % hgs) * kHeads, nh = min(p.G - h0, kHeads);
+    const int h0 = (unit % hgs) * HEADS, nh = min(p.G - h0, HEADS);
     const long long pos = (long long)p.q_offset + i;
     const int ci = (int)(pos / C), ns = p.k + 1, nw = SOLO ? 1 : kWarps * cs, me = SOLO ? 0 : rank * kWarps + warp;
     const int32_t *si = sel_idx + (bg * p.N + i) * p.k;
@@ -128,12 +132,12 @@ __global__ void __launch_bounds__(32 * kWarps, blocks_per_sm(D, C, sizeof(Tout) 
         for (int n = 0; n < RP; ++n) load_pair(std::false_type(), n, c, C - 1);
     }
 
-    // the query rows: lane (r, t) holds head h0 + r at d = 16 c + 4 t .. + 3
-    uint32_t qh[KS][2], ql[QHL ? KS : 1][2];
-    float fq;   // scale log2(e) / the row's power of two, for head r
+    // the query rows: lane (r, t) holds column r, which is head h0 + r (or its second piece), at d = 16 c + 4 t .. + 3
+    uint32_t qf[KS][2];
+    float fq;   // scale log2(e) / the row's power of two, for the head of column r
     {
         float x[KS][4], m = 0.f;
-        const Tin *qr = Q + ((bg * p.G + h0 + min(r, nh - 1)) * p.N + i) * D + 4 * t;
+        const Tin *qr = Q + ((bg * p.G + h0 + min(r % HEADS, nh - 1)) * p.N + i) * D + 4 * t;
 #pragma unroll
         for (int c16 = 0; c16 < KS; ++c16) load4(qr + 16 * c16, x[c16]);
 #pragma unroll
@@ -149,20 +153,21 @@ __global__ void __launch_bounds__(32 * kWarps, blocks_per_sm(D, C, sizeof(Tout) 
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 const float a = x[c16][2 * e] * f, b = x[c16][2 * e + 1] * f;
-                qh[c16][e] = pack_f16(a, b);
+                qf[c16][e] = pack_f16(a, b);
                 if constexpr (QHL) {
-                    const float2 y = unpack_f16(qh[c16][e]);
-                    ql[c16][e] = pack_f16(a - y.x, b - y.y);
+                    const float2 y = unpack_f16(qf[c16][e]);
+                    if (r >= HEADS) qf[c16][e] = pack_f16(a - y.x, b - y.y);
                 }
             }
     }
-    // this lane's columns of the products are heads 2t and 2t + 1
-    const float fq0 = __shfl_sync(0xFFFFFFFFu, fq, 8 * t), fq1 = __shfl_sync(0xFFFFFFFFu, fq, 8 * t + 4);
+    // this lane's columns of the products are heads hd and hd + 1
+    const int hd = 2 * t % HEADS;
+    const float fq0 = __shfl_sync(0xFFFFFFFFu, fq, 4 * hd), fq1 = __shfl_sync(0xFFFFFFFFu, fq, 4 * hd + 4);
 
     // slot factors w_c vs_c over the row's largest, times 2^14; a slot without a chunk has no weight, whatever its score.
     // The loads of all of a warp's heads are in flight together.
     {
-        constexpr int HW = SOLO ? kHeads : kHeads / kWarps;   // heads a warp works out
+        constexpr int HW = SOLO ? HEADS : HEADS / kWarps;   // heads a warp works out
         float s[HW][3], v[3];
 #pragma unroll
         for (int u = 0; u < 3; ++u) {
@@ -249,15 +254,19 @@ __global__ void __launch_bounds__(32 * kWarps, blocks_per_sm(D, C, sizeof(Tout) 
                     for (int u = 0; u < 2; ++u) {
                         if constexpr (PHL) {
                             float x[4] = {0.f, 0.f, 0.f, 0.f};
-                            if constexpr (QHL) mma_bytes(x, w[u][k][0], w[u][k][1], ql[k][0], ql[k][1]);
-                            mma_bytes(x, w[u][k][0], w[u][k][1], qh[k][0], qh[k][1]);
+                            mma_bytes(x, w[u][k][0], w[u][k][1], qf[k][0], qf[k][1]);
                             add4(sacc[m + u], x);
                         } else {
-                            mma_bytes(sacc[m + u], w[u][k][0], w[u][k][1], qh[k][0], qh[k][1]);
-                            if constexpr (QHL) mma_bytes(sacc[m + u], w[u][k][0], w[u][k][1], ql[k][0], ql[k][1]);
+                            mma_bytes(sacc[m + u], w[u][k][0], w[u][k][1], qf[k][0], qf[k][1]);
                         }
                     }
             });
+        if constexpr (QHL) {   // the pieces meet: both lanes of a head go on with the sum
+#pragma unroll
+            for (int m = 0; m < MT; ++m)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) sacc[m][e] += __shfl_xor_sync(0xFFFFFFFFu, sacc[m][e], 2);
+        }
 
         // softmax over the keys seen (those of rows r, r + 8 of each tile, then across the lanes of a column).  Rows of the own
         // chunk that the query does not see hold its last row again: they do not change the maximum and weigh nothing.
@@ -298,7 +307,7 @@ __global__ void __launch_bounds__(32 * kWarps, blocks_per_sm(D, C, sizeof(Tout) 
             l1 += __shfl_xor_sync(0xFFFFFFFFu, l1, o);
         }
         const int slot = OWN ? p.k : turn - 1;
-        const float g0 = __fdividef(s_w[2 * t][slot], l0), g1 = __fdividef(s_w[2 * t + 1][slot], l1);   // 1 <= l <= C
+        const float g0 = __fdividef(s_w[hd][slot], l0), g1 = __fdividef(s_w[hd + 1][slot], l1);   // 1 <= l <= C
 
         // values
 #pragma unroll
@@ -308,14 +317,14 @@ __global__ void __launch_bounds__(32 * kWarps, blocks_per_sm(D, C, sizeof(Tout) 
                 for (int u = 0; u < 2; ++u) {
                     const float(&e)[4] = sacc[m + u];
                     const float x0 = e[0] * g0, x1 = e[1] * g1, x2 = e[2] * g0, x3 = e[3] * g1;
-                    const uint32_t pa = pack_f16(x0, x1), pb = pack_f16(x2, x3);
-                    const uint32_t b0 = movmatrix_t(pa), b1 = movmatrix_t(pb);
-                    [[maybe_unused]] uint32_t r0 = 0u, r1 = 0u;   // what f16 leaves of the probabilities
-                    if constexpr (PHL) {
+                    uint32_t pa = pack_f16(x0, x1), pb = pack_f16(x2, x3);
+                    if constexpr (WIDE) {   // the second columns: what f16 leaves, or nothing
                         const float2 ya = unpack_f16(pa), yb = unpack_f16(pb);
-                        r0 = movmatrix_t(pack_f16(x0 - ya.x, x1 - ya.y));
-                        r1 = movmatrix_t(pack_f16(x2 - yb.x, x3 - yb.y));
+                        const uint32_t ra = PHL ? pack_f16(x0 - ya.x, x1 - ya.y) : 0u, rb = PHL ? pack_f16(x2 - yb.x, x3 - yb.y) : 0u;
+                        pa = t < 2 ? pa : ra;
+                        pb = t < 2 ? pb : rb;
                     }
+                    const uint32_t b0 = movmatrix_t(pa), b1 = movmatrix_t(pb);
 #pragma unroll
                     for (int k = 0; k < KS; k += 2) {
                         uint32_t w[2][2];
@@ -324,7 +333,6 @@ __global__ void __launch_bounds__(32 * kWarps, blocks_per_sm(D, C, sizeof(Tout) 
                         for (int v = 0; v < 2; ++v) {
                             if constexpr (PHL) {
                                 float x[4] = {0.f, 0.f, 0.f, 0.f};
-                                mma_bytes(x, w[v][0], w[v][1], r0, r1);
                                 mma_bytes(x, w[v][0], w[v][1], b0, b1);
                                 add4(oacc[k + v], x);
                             } else {
@@ -345,7 +353,10 @@ __global__ void __launch_bounds__(32 * kWarps, blocks_per_sm(D, C, sizeof(Tout) 
 #pragma unroll
     for (int a = 0; a < KS; ++a)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) part[(2 * t + (e & 1)) * PITCH + 16 * a + r + 8 * (e >> 1)] = oacc[a][e];
+        for (int e = 0; e < 4; ++e) {
+            if constexpr (PHL) oacc[a][e] += __shfl_xor_sync(0xFFFFFFFFu, oacc[a][e], 2);   // both pieces
+            if (!WIDE || t < 2) part[(2 * t + (e & 1)) * PITCH + 16 * a + r + 8 * (e >> 1)] = oacc[a][e];
+        }
     if constexpr (SOLO) {
         __syncwarp();
         for (int e = lane; e < nh * D / 4; e += 32) {
@@ -404,9 +415,9 @@ struct Share {
     double time;
 };
 
-Share share_of(const Dims &p, int per_sm)
+Share share_of(const Dims &p, int per_sm, int heads)
 {
-    const double rows = (double)p.B * p.Hkv * ((p.G + kHeads - 1) / kHeads) * p.N, blocks = 148.0 * per_sm;
+    const double rows = (double)p.B * p.Hkv * ((p.G + heads - 1) / heads) * p.N, blocks = 148.0 * per_sm;
     // slots that can hold a chunk: no more than the last query has chunks before its own
     const int ns = (int)fmin(p.k, ((double)p.q_offset + p.N - 1) / p.C) + 1;
     auto rounds = [](double x) { return x <= 1.0 ? 1.0 : x <= 4.0 ? ceil(x) + 0.25 : x + 0.5; };
@@ -424,8 +435,9 @@ template <typename Tin, typename Tout, int D, int C>
 cudaError_t launch_t(const Dims &p, const void *Q, const uint8_t *K8, const uint8_t *V8, const float *ks, const float *vs,
                      const int32_t *sel_idx, const float *sel_score, void *O, cudaStream_t s)
 {
-    const int hgs = (p.G + kHeads - 1) / kHeads;
-    const int cs = share_of(p, blocks_per_sm(D, C, sizeof(Tout) == 4)).cs;
+    constexpr int heads = heads_of(sizeof(Tin) == 4 || sizeof(Tout) == 4);
+    const int hgs = (p.G + heads - 1) / heads;
+    const int cs = share_of(p, blocks_per_sm(D, C, sizeof(Tout) == 4), heads).cs;
     const long long units = (long long)p.N * hgs;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(cs ? units * cs : (units + kWarps - 1) / kWarps), (unsigned)(p.B * p.Hkv));
@@ -475,7 +487,7 @@ static bool use_union(const Dims &p, hils_dtype in, hils_dtype out)
     const double U = V * (1.0 - pow(1.0 - fmin(1.0, p.k / V), BQ)) + BQ / p.C + 1.0;
     const double blocks = (double)p.B * p.Hkv * ((p.N + BQ - 1) / BQ) / 148.0;
     const double t_union = (blocks <= 1.0 ? 1.0 : blocks + 0.5) * (5.0 + 0.8 * fmin(U, V + 1.0));
-    return t_union < 1.9 * share_of(p, blocks_per_sm(p.d, p.C, false)).time;
+    return t_union < 1.9 * share_of(p, blocks_per_sm(p.d, p.C, false), heads_of(false)).time;
 }
 
 cudaError_t launch_attend8(const Dims &p, hils_dtype in, hils_dtype out, const void *Q, const uint8_t *K8,
