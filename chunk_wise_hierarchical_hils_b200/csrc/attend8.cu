@@ -409,7 +409,7 @@ __global__ void __launch_bounds__(32 * kWarps, blocks_per_sm(D, C, sizeof(Tout) 
 // often the resident warps start over.  8 rows of 65 slots go to teams of eight blocks (8.5 us; six 8.8, four 10.6),
 // 128 rows of 33 slots to teams of three (17.1 us; two 17.9, four, which queue, 24), 4072 rows of 33 slots to single
 // blocks (188 us; lone warps 190, pairs 263), 65536 rows of 17 slots and 2006 rows of 5 to lone warps (1.35 ms and 11 us;
-// blocks 1.65 ms and 16 us; all measured before the last few percent of the kernel's time went).
+// blocks 1.65 ms and 16 us).
 struct Share {
     int cs;
     double time;

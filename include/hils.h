@@ -331,7 +331,9 @@ HILS_API hils_status hils_cache_read_q8(const hils_problem *p, const void *K8, c
  * hils_landmarks from the 8-bit keys: L and beta of chunks [c_begin, c_end) from
  * the chunk's rows below t_end, the number of tokens in the cache (1 <= t_end
  * <= T, c_end <= ceil(t_end / C), so that every chunk asked for holds a row).
- * U [B][Hkv][nL][d] and L [B][Hkv][nL][d] in in_dtype, beta float or NULL.
+ * U [B][Hkv][nL][d] and L [B][Hkv][nL][d] in in_dtype, beta [B][Hkv][nL]
+ * float or NULL; rows of other chunks are not written, and L must not overlap
+ * K8 or U.  Uses B, Hkv, T, d, C, in_dtype and scale of p.
  * A decode step that completes chunk c calls it with c, c + 1, (c + 1) * C.
  */
 HILS_API hils_status hils_landmarks_q8(const hils_problem *p, const void *K8, const float *k_scale, const void *U,
