@@ -748,7 +748,7 @@ hils_status hils_chunk_attend_fuse_q8_workspace_size(const hils_problem *p, size
     if (!bytes) return HILS_ERR_INVALID_ARG;
     const hils_status st = resolve(p, &d);
     if (st != HILS_OK) return st;
-    *bytes = attend8_ws_bytes(d, p->in_dtype, p->out_dtype);
+    *bytes = 0;   // partial results meet in shared memory
     return HILS_OK;
 }
 
@@ -764,8 +764,8 @@ hils_status hils_chunk_attend_fuse_q8(const hils_problem *p, const void *Q, cons
     if (!aligned16(Q) || !aligned_cache8(K8, V8, k_scale, v_scale) || !aligned16(O) || !aligned16(sel_score) ||
         (sel_idx && !aligned16(sel_idx)))
         return HILS_ERR_INVALID_ARG;
-    st = check_ws(workspace, workspace_bytes, attend8_ws_bytes(d, p->in_dtype, p->out_dtype));
-    if (st != HILS_OK) return st;
+    (void)workspace;   // none is needed
+    (void)workspace_bytes;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (check_caller_selection()) {
         st = check_selection(d, sel_idx, s);
@@ -775,8 +775,7 @@ hils_status hils_chunk_attend_fuse_q8(const hils_problem *p, const void *Q, cons
     st = device_ctl(&ctl);
     if (st != HILS_OK) return st;
     return from_cuda(launch_attend8(d, p->in_dtype, p->out_dtype, Q, static_cast<const uint8_t *>(K8),
-                                    static_cast<const uint8_t *>(V8), k_scale, v_scale, sel_idx, sel_score, O, workspace,
-                                    ctl, s));
+                                    static_cast<const uint8_t *>(V8), k_scale, v_scale, sel_idx, sel_score, O, ctl, s));
 }
 
 hils_status hils_forward_q8_workspace_size(const hils_problem *p, size_t *bytes)
@@ -785,8 +784,7 @@ hils_status hils_forward_q8_workspace_size(const hils_problem *p, size_t *bytes)
     if (!bytes) return HILS_ERR_INVALID_ARG;
     const hils_status st = resolve(p, &d);
     if (st != HILS_OK) return st;
-    const size_t sel = select_ws(d), att = attend8_ws_bytes(d, p->in_dtype, p->out_dtype);
-    *bytes = sel_idx_bytes(d) + sel_score_bytes(d) + (sel > att ? sel : att);
+    *bytes = sel_idx_bytes(d) + sel_score_bytes(d) + select_ws(d);
     return HILS_OK;
 }
 
@@ -815,8 +813,7 @@ hils_status hils_forward_q8(const hils_problem *p, const void *Q, const void *K8
     st = device_ctl(&ctl);
     if (st != HILS_OK) return st;
     return from_cuda(launch_attend8(d, p->in_dtype, p->out_dtype, Q, static_cast<const uint8_t *>(K8),
-                                    static_cast<const uint8_t *>(V8), k_scale, v_scale, sel_idx, sel_score, O, scratch, ctl,
-                                    s));
+                                    static_cast<const uint8_t *>(V8), k_scale, v_scale, sel_idx, sel_score, O, ctl, s));
 }
 
 hils_status hils_sync_status(void *stream)

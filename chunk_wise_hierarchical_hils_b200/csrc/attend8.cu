@@ -470,8 +470,6 @@ cudaError_t launch_d(const Dims &p, const void *Q, const uint8_t *K8, const uint
 
 }  // namespace
 
-size_t attend8_ws_bytes(const Dims &, hils_dtype, hils_dtype) { return 0; }
-
 // Test control: HILS_Q8_KERNEL=rows or =union forces the kernel (the latter where it covers the shape).
 static bool use_union(const Dims &p, hils_dtype in, hils_dtype out)
 {
@@ -492,7 +490,7 @@ static bool use_union(const Dims &p, hils_dtype in, hils_dtype out)
 
 cudaError_t launch_attend8(const Dims &p, hils_dtype in, hils_dtype out, const void *Q, const uint8_t *K8,
                            const uint8_t *V8, const float *ks, const float *vs, const int32_t *sel_idx,
-                           const float *sel_score, void *O, void *, const DeviceCtl &ctl, cudaStream_t s)
+                           const float *sel_score, void *O, const DeviceCtl &ctl, cudaStream_t s)
 {
     if (use_union(p, in, out)) return launch_attend8_tc(p, Q, K8, V8, ks, vs, sel_idx, sel_score, O, ctl, s);
     if (in == HILS_F32)

@@ -26,9 +26,8 @@ bool attend8_tc_supported(const Dims &p, hils_dtype in, hils_dtype out);
 cudaError_t launch_attend8_tc(const Dims &p, const void *Q, const uint8_t *K8, const uint8_t *V8, const float *ks,
                               const float *vs, const int32_t *sel_idx, const float *sel_score, void *O,
                               const DeviceCtl &ctl, cudaStream_t s);
-size_t attend8_ws_bytes(const Dims &p, hils_dtype in, hils_dtype out);
 cudaError_t launch_attend8(const Dims &p, hils_dtype in, hils_dtype out, const void *Q, const uint8_t *K8,
                            const uint8_t *V8, const float *ks, const float *vs, const int32_t *sel_idx,
-                           const float *sel_score, void *O, void *ws, const DeviceCtl &ctl, cudaStream_t s);
+                           const float *sel_score, void *O, const DeviceCtl &ctl, cudaStream_t s);
 
 }  // namespace hils
