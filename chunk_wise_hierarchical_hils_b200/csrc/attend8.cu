@@ -42,6 +42,7 @@ namespace {
 using namespace t8;
 
 constexpr int kWarps = 4;
+constexpr int kMaxTeam = 8;    // blocks of a cluster that share a row (the portable limit)
 constexpr int kCols = 8;       // columns of a product
 // Heads a row of work covers: one a column; with float32 queries or results four, whose second pieces take the others.
 constexpr int heads_of(bool wide) { return wide ? 4 : 8; }
@@ -381,8 +382,12 @@ __global__ void __launch_bounds__(32 * kWarps, blocks_per_sm(D, C, sizeof(Tout) 
             for (int e = rank * 32 * kWarps + tid; e < nh * D; e += cs * 32 * kWarps) {
                 const int h = e / D, x = e % D;
                 const uint32_t addr = sm100::smem_addr(sum + h * PITCH + x);
-                float a = 0.f;
-                for (int k = 0; k < cs; ++k) a += ld_cluster(addr, (uint32_t)k);
+                // all the blocks' shares are asked for before the first is added
+                float v[kMaxTeam], a = 0.f;
+#pragma unroll
+                for (int k = 0; k < kMaxTeam; ++k) v[k] = k < cs ? ld_cluster(addr, (uint32_t)k) : 0.f;
+#pragma unroll
+                for (int k = 0; k < kMaxTeam; ++k) a += v[k];
                 store_out(O + ((bg * p.G + h0 + h) * p.N + i) * D + x, a * s_top[h]);
             }
             cluster_sync();   // the others' reads of this block's rows
@@ -422,7 +427,7 @@ Share share_of(const Dims &p, int per_sm, int heads)
     const int ns = (int)fmin(p.k, ((double)p.q_offset + p.N - 1) / p.C) + 1;
     auto rounds = [](double x) { return x <= 1.0 ? 1.0 : x <= 4.0 ? ceil(x) + 0.25 : x + 0.5; };
     Share best = {0, rounds(rows / (blocks * kWarps)) * (ns + 3.0)};
-    for (int cs = 1; cs <= 8; ++cs) {
+    for (int cs = 1; cs <= kMaxTeam; ++cs) {
         const int w = kWarps * cs;
         const double turns = 0.5 * ((ns + w - 1) / w + (double)ns / w);
         const double t = rounds(rows * cs / blocks) * (turns + 1.5);
