@@ -49,17 +49,27 @@ constexpr int heads_of(bool wide) { return wide ? 4 : 8; }
 constexpr int kMaxSlots = HILS_MAX_K + 1;
 
 __device__ __forceinline__ uint32_t cluster_rank() { uint32_t r; asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r)); return r; }
-__device__ __forceinline__ void cluster_sync()
-{
-    asm volatile("barrier.cluster.arrive.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
-}
-__device__ __forceinline__ float ld_cluster(uint32_t addr, uint32_t rank)
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.aligned;" ::: "memory"); }
+// v to `addr` (an address of this block's shared memory) of the cluster's block `rank`
+__device__ __forceinline__ void st_cluster(uint32_t addr, uint32_t rank, float4 v)
 {
     uint32_t a;
-    float v;
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(addr), "r"(rank));
-    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(a) : "memory");
-    return v;
+    asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(a), "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w) : "memory");
+}
+
+// Largest of the warp's values in one integer reduction; the first for any values, the second for values that are not
+// negative.
+__device__ __forceinline__ float redux_max(float x)
+{
+    const uint32_t u = __float_as_uint(x);
+    const uint32_t k = __reduce_max_sync(0xFFFFFFFFu, (u & 0x80000000u) ? ~u : u | 0x80000000u);
+    return __uint_as_float((k & 0x80000000u) ? k & 0x7FFFFFFFu : ~k);
+}
+__device__ __forceinline__ float redux_max_pos(float x)
+{
+    return __uint_as_float(__reduce_max_sync(0xFFFFFFFFu, __float_as_uint(x)));
 }
 
 // Blocks an SM holds: by registers, and for d = 128 by 16 KB of ring a warp.
@@ -90,11 +100,13 @@ __global__ void __launch_bounds__(32 * kWarps, blocks_per_sm(D, C, sizeof(Tout) 
     __shared__ float s_weights[ROWS][HEADS][kMaxSlots];
     __shared__ float s_tops[ROWS][HEADS];
     __shared__ int s_chunks[ROWS][kMaxSlots];
+    __shared__ __align__(16) float s_shares[SOLO ? 4 : HEADS * D + 4 * kMaxTeam];   // [block of the cluster][slice]
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, r = lane >> 2, t = lane & 3;
     const int rank = !SOLO && cs > 1 ? (int)cluster_rank() : 0;
     const int unit = SOLO ? blockIdx.x * kWarps + warp : blockIdx.x / cs, i = unit / hgs;
     if (SOLO && i >= p.N) return;                     // whole warps leave; a block of lone warps has no barrier
+    if (!SOLO && cs > 1) cluster_arrive();            // waited for before the first access to another block
     float (&s_w)[HEADS][kMaxSlots] = s_weights[SOLO ? warp : 0];
     float (&s_top)[HEADS] = s_tops[SOLO ? warp : 0];
     int (&s_chunk)[kMaxSlots] = s_chunks[SOLO ? warp : 0];
@@ -114,15 +126,38 @@ __global__ void __launch_bounds__(32 * kWarps, blocks_per_sm(D, C, sizeof(Tout) 
         cp_commit();
     };
 
+    // Everything the start needs and knows the place of is asked for first: the row's slots and its heads' scores (lane l
+    // holds slots l, l + 32, l + 64), the query rows.
+    constexpr int HW = SOLO ? HEADS : HEADS / kWarps;   // heads whose weights this warp works out
+    int cc[3];
+    float s[HW][3], x[KS][4];
+#pragma unroll
+    for (int u = 0; u < 3; ++u) cc[u] = lane + 32 * u < p.k ? __ldg(si + lane + 32 * u) : -1;
+#pragma unroll
+    for (int u = 0; u < 3; ++u)
+#pragma unroll
+        for (int q = 0; q < HW; ++q) {
+            const int h = SOLO ? q : warp + q * kWarps;
+            s[q][u] = lane + 32 * u < ns && h < nh
+                          ? __ldg(sel_score + ((bg * p.G + h0 + h) * p.N + i) * ns + lane + 32 * u) : -INFINITY;
+        }
+    {
+        const Tin *qr = Q + ((bg * p.G + h0 + min(r % HEADS, nh - 1)) * p.N + i) * D + 4 * t;
+#pragma unroll
+        for (int c16 = 0; c16 < KS; ++c16) load4(qr + 16 * c16, x[c16]);
+    }
+    // An entry that is no past chunk of the query is an empty slot: nothing outside the cache is read for it.
+#pragma unroll
+    for (int u = 0; u < 3; ++u) {
+        const int jj = lane + 32 * u;
+        cc[u] = jj == p.k ? ci : (unsigned)cc[u] < (unsigned)ci ? cc[u] : -1;
+        if ((SOLO || warp == 0) && jj < ns) s_chunk[jj] = cc[u];
+    }
+    auto chunk_of = [&](int j) { return __shfl_sync(0xFFFFFFFFu, j < 32 ? cc[0] : j < 64 ? cc[1] : cc[2], j & 31); };
+
     // The own chunk, whose rows behind the query are not seen, is the first in the order of work and past chunks (whole
     // ones) follow: turn 0 is slot k, turn x > 0 slot x - 1.  This warp's turns are me, me + nw, ..
-    // An entry that is no past chunk of the query is an empty slot: nothing outside the cache is read for it.
-    auto chunk_of = [&](int j) {
-        if (j >= p.k) return j == p.k ? ci : -1;
-        const int x = __ldg(si + j);
-        return (unsigned)x < (unsigned)ci ? x : -1;
-    };
-    int turn = me, c = turn == 0 ? ci : chunk_of(turn <= p.k ? turn - 1 : ns);
+    int turn = me, c = turn == 0 ? ci : turn <= p.k ? chunk_of(turn - 1) : -1;
     while (c < 0 && turn + nw < ns) { turn += nw; c = chunk_of(turn - 1); }
     const int own_top = (int)(pos - (long long)ci * C);
     if (turn == 0) {
@@ -132,15 +167,15 @@ __global__ void __launch_bounds__(32 * kWarps, blocks_per_sm(D, C, sizeof(Tout) 
 #pragma unroll
         for (int n = 0; n < RP; ++n) load_pair(std::false_type(), n, c, C - 1);
     }
+    float v[3];
+#pragma unroll
+    for (int u = 0; u < 3; ++u) v[u] = cc[u] >= 0 ? __ldg(vs + bg * p.nL + cc[u]) : 0.f;
 
     // the query rows: lane (r, t) holds column r, which is head h0 + r (or its second piece), at d = 16 c + 4 t .. + 3
     uint32_t qf[KS][2];
     float fq;   // scale log2(e) / the row's power of two, for the head of column r
     {
-        float x[KS][4], m = 0.f;
-        const Tin *qr = Q + ((bg * p.G + h0 + min(r % HEADS, nh - 1)) * p.N + i) * D + 4 * t;
-#pragma unroll
-        for (int c16 = 0; c16 < KS; ++c16) load4(qr + 16 * c16, x[c16]);
+        float m = 0.f;
 #pragma unroll
         for (int c16 = 0; c16 < KS; ++c16)
             m = fmaxf(m, fmaxf(fmaxf(fabsf(x[c16][0]), fabsf(x[c16][1])), fmaxf(fabsf(x[c16][2]), fabsf(x[c16][3]))));
@@ -165,22 +200,8 @@ __global__ void __launch_bounds__(32 * kWarps, blocks_per_sm(D, C, sizeof(Tout) 
     const int hd = 2 * t % HEADS;
     const float fq0 = __shfl_sync(0xFFFFFFFFu, fq, 4 * hd), fq1 = __shfl_sync(0xFFFFFFFFu, fq, 4 * hd + 4);
 
-    // slot factors w_c vs_c over the row's largest, times 2^14; a slot without a chunk has no weight, whatever its score.
-    // The loads of all of a warp's heads are in flight together.
+    // slot factors w_c vs_c over the row's largest, times 2^14; a slot without a chunk has no weight, whatever its score
     {
-        constexpr int HW = SOLO ? HEADS : HEADS / kWarps;   // heads a warp works out
-        float s[HW][3], v[3];
-#pragma unroll
-        for (int u = 0; u < 3; ++u) {
-            const int jj = lane + 32 * u, cc = chunk_of(jj);
-            v[u] = cc >= 0 ? __ldg(vs + bg * p.nL + cc) : 0.f;
-            if ((SOLO || warp == 0) && jj < ns) s_chunk[jj] = cc;
-#pragma unroll
-            for (int q = 0; q < HW; ++q) {
-                const int h = SOLO ? q : warp + q * kWarps;
-                s[q][u] = cc >= 0 && h < nh ? __ldg(sel_score + ((bg * p.G + h0 + h) * p.N + i) * ns + jj) : -INFINITY;
-            }
-        }
 #pragma unroll
         for (int q = 0; q < HW; ++q) {
             const int h = SOLO ? q : warp + q * kWarps;
@@ -188,7 +209,9 @@ __global__ void __launch_bounds__(32 * kWarps, blocks_per_sm(D, C, sizeof(Tout) 
                 for (int jj = lane; jj < ns; jj += 32) s_w[h][jj] = 0.f;
                 continue;
             }
-            const float mx = warp_max(fmaxf(fmaxf(s[q][0], s[q][1]), s[q][2]));
+#pragma unroll
+            for (int u = 0; u < 3; ++u) s[q][u] = cc[u] >= 0 ? s[q][u] : -INFINITY;
+            const float mx = redux_max(fmaxf(fmaxf(s[q][0], s[q][1]), s[q][2]));
             float z = 0.f, top = 0.f;
 #pragma unroll
             for (int u = 0; u < 3; ++u) {
@@ -202,7 +225,7 @@ __global__ void __launch_bounds__(32 * kWarps, blocks_per_sm(D, C, sizeof(Tout) 
                 s[q][u] = s[q][u] == 0.f ? 0.f : s[q][u] * iz * v[u];
                 top = fmaxf(top, s[q][u]);
             }
-            top = warp_max(top);
+            top = redux_max_pos(top);
             if (top > 0.f) top = fmaxf(top, 1e-34f);   // its inverse stays finite
             const float f = top > 0.f ? 16384.0f / top : 1.0f;
 #pragma unroll
@@ -370,41 +393,47 @@ __global__ void __launch_bounds__(32 * kWarps, blocks_per_sm(D, C, sizeof(Tout) 
         // the warps' rows, and a cluster's, are added in order
         __syncthreads();
         float *sum = reinterpret_cast<float *>(s_ring);
-        if (cs > 1) {
-            for (int e = tid; e < nh * D; e += 32 * kWarps) {
-                float *at = sum + e / D * PITCH + e % D;
-                float a = at[0];
-#pragma unroll
-                for (int w = 1; w < kWarps; ++w) a += at[w * (SPACE / 4)];
-                at[0] = a;
-            }
-            cluster_sync();
-            for (int e = rank * 32 * kWarps + tid; e < nh * D; e += cs * 32 * kWarps) {
-                const int h = e / D, x = e % D;
-                const uint32_t addr = sm100::smem_addr(sum + h * PITCH + x);
-                // all the blocks' shares are asked for before the first is added
-                float v[kMaxTeam], a = 0.f;
-#pragma unroll
-                for (int k = 0; k < kMaxTeam; ++k) v[k] = k < cs ? ld_cluster(addr, (uint32_t)k) : 0.f;
-#pragma unroll
-                for (int k = 0; k < kMaxTeam; ++k) a += v[k];
-                store_out(O + ((bg * p.G + h0 + h) * p.N + i) * D + x, a * s_top[h]);
-            }
-            cluster_sync();   // the others' reads of this block's rows
-            return;
-        }
-        for (int e = tid; e < nh * D / 4; e += 32 * kWarps) {
-            const int h = e / (D / 4), x = e % (D / 4) * 4;
-            const float *at = sum + h * PITCH + x;
+        auto block_sum = [&](int e) {   // elements 4 e .. 4 e + 3 of the rows
+            const float *at = sum + e / (D / 4) * PITCH + e % (D / 4) * 4;
             float4 a = *reinterpret_cast<const float4 *>(at);
 #pragma unroll
             for (int w = 1; w < kWarps; ++w) {
-                const float4 v = *reinterpret_cast<const float4 *>(at + w * (SPACE / 4));
-                a = make_float4(a.x + v.x, a.y + v.y, a.z + v.z, a.w + v.w);
+                const float4 y = *reinterpret_cast<const float4 *>(at + w * (SPACE / 4));
+                a = make_float4(a.x + y.x, a.y + y.y, a.z + y.z, a.w + y.w);
             }
+            return a;
+        };
+        auto store = [&](int e, float4 a) {
+            const int h = e / (D / 4), y = e % (D / 4) * 4;
             const float f = s_top[h];
-            store4(O + ((bg * p.G + h0 + h) * p.N + i) * D + x, make_float4(a.x * f, a.y * f, a.z * f, a.w * f));
+            store4(O + ((bg * p.G + h0 + h) * p.N + i) * D + y, make_float4(a.x * f, a.y * f, a.z * f, a.w * f));
+        };
+        const int n4 = nh * D / 4;
+        if (cs > 1) {
+            // Every block of the cluster finishes a slice of the rows: the others send it their sums of that slice.  One
+            // barrier: nothing of a block is accessed by others behind it.
+            const int slice = (n4 + cs - 1) / cs;
+            cluster_wait();   // all blocks have started
+            for (int e = tid; e < n4; e += 32 * kWarps) {
+                const int to = e / slice;
+                st_cluster(sm100::smem_addr(&s_shares[4 * (rank * slice + e - to * slice)]), (uint32_t)to, block_sum(e));
+            }
+            __syncwarp();
+            cluster_arrive();
+            cluster_wait();
+            for (int e = tid; e < slice && rank * slice + e < n4; e += 32 * kWarps) {
+                float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                for (int k = 0; k < kMaxTeam; ++k)
+                    if (k < cs) {
+                        const float4 y = *reinterpret_cast<const float4 *>(&s_shares[4 * (k * slice + e)]);
+                        a = make_float4(a.x + y.x, a.y + y.y, a.z + y.z, a.w + y.w);
+                    }
+                store(rank * slice + e, a);
+            }
+            return;
         }
+        for (int e = tid; e < n4; e += 32 * kWarps) store(e, block_sum(e));
     }
 }
 
