@@ -440,10 +440,10 @@ __global__ void __launch_bounds__(32 * kWarps, blocks_per_sm(D, C, sizeof(Tout) 
 // How the rows are shared out: cs = 0: a warp a row (SOLO), else teams of cs blocks; and the time it is expected to
 // take, in the time of a warp's chunk (1.9 us with every SM full).  Weighed: a warp's turns of its row (the longest
 // list and the mean), the start and end of a row (3 chunks for a lone warp, 1.5 for a team, its merge included), and how
-// often the resident warps start over.  8 rows of 65 slots go to teams of eight blocks (8.5 us; six 8.8, four 10.6),
-// 128 rows of 33 slots to teams of three (17.1 us; two 17.9, four, which queue, 24), 4072 rows of 33 slots to single
-// blocks (188 us; lone warps 190, pairs 263), 65536 rows of 17 slots and 2006 rows of 5 to lone warps (1.35 ms and 11 us;
-// blocks 1.65 ms and 16 us).
+// often the resident warps start over.  Measured side by side: 8 rows of 65 slots, teams of eight blocks 8.5 us, six 8.8,
+// four 10.6; 128 rows of 33 slots, teams of three 17.1 us, two 17.9, four, which queue, 24; 4072 rows of 33 slots, single
+// blocks 188 us, lone warps 190, pairs 263; 65536 rows of 17 slots and 2006 rows of 5, lone warps 1.35 ms and 11 us, blocks
+// 1.65 ms and 16 us.
 struct Share {
     int cs;
     double time;
@@ -514,7 +514,7 @@ static bool use_union(const Dims &p, hils_dtype in, hils_dtype out)
     // The union's cost is known only for selections that have nothing to do with one another, its worst case: of V
     // visible chunks a block's BQ queries then want V (1 - (1 - k / V)^BQ).  A chunk of it takes 0.8 us and a
     // block's set-up 5 us (8K prefill, 62 chunks on average: 810 us against 1.32 ms by rows; 509 queries at 130K, 810 chunks
-    // a block of which a query wants 33: 474 us against 189).
+    // a block of which a query wants 33: 474 us against 184).
     const double BQ = 128 / p.G, V = (p.q_offset + 0.5 * p.N) / p.C + 1.0;
     const double U = V * (1.0 - pow(1.0 - fmin(1.0, p.k / V), BQ)) + BQ / p.C + 1.0;
     const double blocks = (double)p.B * p.Hkv * ((p.N + BQ - 1) / BQ) / 148.0;
