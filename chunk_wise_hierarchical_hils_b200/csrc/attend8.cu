@@ -259,7 +259,11 @@ __global__ void __launch_bounds__(32 * kWarps, blocks_per_sm(D, C, sizeof(Tout) 
             else cp_commit();   // groups are counted
         };
         const float kc = __ldg(ks + bg * p.nL + c);
-        const float f0 = fq0 * kc, f1 = fq1 * kc;
+        const int slot = OWN ? p.k : turn - 1;
+        // a head that gives the slot no weight takes its logits as zeros: their factor may be beyond float32, and a NaN would
+        // reach the head's row through the weight of zero
+        const float w0 = s_w[hd][slot], w1 = s_w[hd + 1][slot];
+        const float f0 = w0 == 0.f ? 0.f : fq0 * kc, f1 = w1 == 0.f ? 0.f : fq1 * kc;
 
         // scores, two tiles of keys at a time: their products are independent of one another
         float sacc[MT][4];
@@ -330,8 +334,7 @@ __global__ void __launch_bounds__(32 * kWarps, blocks_per_sm(D, C, sizeof(Tout) 
             l0 += __shfl_xor_sync(0xFFFFFFFFu, l0, o);
             l1 += __shfl_xor_sync(0xFFFFFFFFu, l1, o);
         }
-        const int slot = OWN ? p.k : turn - 1;
-        const float g0 = __fdividef(s_w[hd][slot], l0), g1 = __fdividef(s_w[hd + 1][slot], l1);   // 1 <= l <= C
+        const float g0 = __fdividef(w0, l0), g1 = __fdividef(w1, l1);   // 1 <= l <= C
 
         // values
 #pragma unroll

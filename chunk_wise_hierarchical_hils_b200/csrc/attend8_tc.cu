@@ -498,8 +498,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             uint32_t pk[32];
             if (__any_sync(0xFFFFFFFFu, w != 0.f)) {   // rows with w = 0 get P = 0 from the scaling
                 const int n_vis = (c == own && valid) ? (int)(pos - (long long)c * kChunk + 1) : left;
-                // a factor too small for float32 makes every logit the same number: the smallest normal one does that too
-                chunk_softmax_row<kPolyPairEvery>(sv, n_vis, w, fmaxf(fq * kc, 1.2e-38f), pk);
+                // a factor too small for float32 makes every logit the same number: the smallest normal one does that too.
+                // A row without weight takes that one: its own may be beyond float32, and a NaN would outlive w = 0
+                const float f = w == 0.f ? 0.f : fq * kc;
+                chunk_softmax_row<kPolyPairEvery>(sv, n_vis, w, fmaxf(f, 1.2e-38f), pk);
             } else {
 #pragma unroll
                 for (int j = 0; j < 32; ++j) pk[j] = 0u;
