@@ -166,6 +166,16 @@ __device__ __forceinline__ void store_values(float *out, uint32_t b, float s)
     *reinterpret_cast<float4 *>(out) = make_float4(v[0] * s, v[1] * s, v[2] * s, v[3] * s);
 }
 
+// A product has up to 28 bits (4 of the value) and bf16 keeps 8: it is rounded once where float32 holds it exactly, which
+// is so for scales whose last four bits are zero (what an append writes has none set), down to 2^-117 (2^-9 of which is
+// float32's smallest normal number).  With any other scale it is taken in 64 bits, behind a branch: chosen element by
+// element both were computed (128K tokens 169 us against 120).
+__device__ __forceinline__ bool exact_products(float s)
+{
+    const uint32_t u = __float_as_uint(s);
+    return (u & 15u) == 0u && ((u >> 23) & 255u) >= 127u - 117u;
+}
+
 __device__ __forceinline__ void store_values(__nv_bfloat16 *out, uint2 b, float s)
 {
     float v[8];
@@ -173,10 +183,19 @@ __device__ __forceinline__ void store_values(__nv_bfloat16 *out, uint2 b, float 
     e4m3x4_to_float(b.y, v + 4);
     uint4 u;
     uint32_t *w = reinterpret_cast<uint32_t *>(&u);
+    if (exact_products(s)) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        const __nv_bfloat162 t = __floats2bfloat162_rn(v[2 * j] * s, v[2 * j + 1] * s);
-        w[j] = *reinterpret_cast<const uint32_t *>(&t);
+        for (int j = 0; j < 4; ++j) {
+            const __nv_bfloat162 t = __floats2bfloat162_rn(v[2 * j] * s, v[2 * j + 1] * s);
+            w[j] = *reinterpret_cast<const uint32_t *>(&t);
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const __nv_bfloat162 t = __halves2bfloat162(__double2bfloat16((double)v[2 * j] * s),
+                                                        __double2bfloat16((double)v[2 * j + 1] * s));
+            w[j] = *reinterpret_cast<const uint32_t *>(&t);
+        }
     }
     *reinterpret_cast<uint4 *>(out) = u;
 }

@@ -1,9 +1,11 @@
-"""The 8-bit cache's attention where a weight is zero and the numbers behind it are not: what a row gives no weight to must
-not reach its result, however large the products with it would be."""
+"""The 8-bit cache where the numbers are unusual: what a row gives no weight to does not reach its result, however large the
+products with it would be, and a value read back is rounded once, whatever its scale."""
 import numpy as np
 import pytest
 import torch
 
+import cache8_ref as ref
+import chunk_wise_hierarchical_hils_b200 as hils
 import test_cache8_gpu as c8
 
 pytestmark = pytest.mark.gpu
@@ -64,3 +66,37 @@ def test_heads_far_apart_with_slots_of_their_own(N, kernel, dtype, out, monkeypa
     O = c8.attend(p, dev)
     c8.ok()
     c8.compare(p, h, O, out)
+
+
+def bf16_nearest(x):
+    """float64 rounded once to bf16's 8 significant bits (halves to even; subnormals in steps of 2^-133)."""
+    _, e = np.frexp(x)
+    step = np.ldexp(1.0, np.maximum(e, -125) - 8)
+    return np.rint(x / step) * step
+
+
+def test_read_rounds_once():
+    """Scales of 24 bits: scale * value has up to 28 and is rounded to bf16 from all of them.  The scales are chosen so that a
+    product lies next to the middle between two bf16 numbers, closer than float32 tells apart."""
+    r = np.random.default_rng(620)
+    B, Hkv, T, d, C = 1, 2, 1 << 13, 64, 32
+    nL = T // C
+    data = [r.integers(0, 256, (B, Hkv, T, d), dtype=np.uint8) for _ in range(2)]
+    middle = [(2 * r.integers(128, 256, (B, Hkv, nL)) + 1) / r.integers(9, 16, (B, Hkv, nL)) for _ in range(2)]
+    scale = [(m * 2.0 ** r.integers(-20, 20, (B, Hkv, nL))).astype(np.float32) for m in middle]
+    scale[1][:, :, ::4] *= np.float32(2.0 ** -112)                  # results at and below the smallest normal number
+    scale[1][:, :, 1::4] = (r.uniform(1.0, 2.0, scale[1][:, :, 1::4].shape) * 2.0 ** -135).astype(np.float32)
+    want = [ref.TABLE[x] * s.astype(np.float64)[:, :, np.arange(T) // C, None] for x, s in zip(data, scale)]
+    nan = [np.isnan(w) for w in want]
+    once = [bf16_nearest(np.where(n, 0.0, w)) for w, n in zip(want, nan)]
+    twice = [torch.from_numpy(np.where(n, 0.0, w).astype(np.float32)).to(torch.bfloat16).double().numpy() for w, n in zip(want, nan)]
+    assert all(np.any(a != b) for a, b in zip(once, twice))
+    p = hils.problem(B, Hkv, Hkv, 1, T, d, C, 0, 0, hils.HILS_BF16)
+    out = [torch.empty((B, Hkv, T, d), dtype=torch.bfloat16, device=c8.DEV) for _ in range(2)]
+    dd, sd = [torch.from_numpy(x).to(c8.DEV) for x in data], [torch.from_numpy(x).to(c8.DEV) for x in scale]
+    hils.hils_cache_read_q8(p, dd[0], dd[1], sd[0], sd[1], out[0], out[1], 0, T)
+    c8.ok()
+    for side in range(2):
+        got = out[side].double().cpu().numpy()
+        assert np.all(np.isnan(got[nan[side]]))
+        assert np.array_equal(np.where(nan[side], 0.0, got), once[side])
