@@ -514,6 +514,7 @@ static bool use_union(const Dims &p, hils_dtype in, hils_dtype out)
     const char *force = getenv("HILS_Q8_KERNEL");
     if (force && strcmp(force, "rows") == 0) return false;
     if (force && strcmp(force, "union") == 0) return true;
+    if (!attend8_tc_fits(p)) return false;
     // The union's cost is known only for selections that have nothing to do with one another, its worst case: of V
     // visible chunks a block's BQ queries then want V (1 - (1 - k / V)^BQ).  A chunk of it takes 0.8 us and a
     // block's set-up 5 us (8K prefill, 62 chunks on average: 810 us against 1.32 ms by rows; 509 queries at 130K, 810 chunks

@@ -32,6 +32,10 @@
 // warps take 128 (the sum of the shares is what the block was launched with, which the host checks).
 #include <cuda.h>
 #include <cuda_fp16.h>
+#include <stdlib.h>
+#include <string.h>
+
+#include <atomic>
 
 #include "cache8.h"
 #include "chunk_softmax.cuh"
@@ -557,6 +561,27 @@ uint32_t smem_bytes(const Dims &p)
     return make_layout(p.k, c_max / 32 + 1, kRows / p.G).total + 1024;
 }
 
+// The warps' register shares are drawn from what the block is launched with: a build whose kernel has another number of
+// registers would wait for them forever, and does not run it.  A query of the number that fails is made again by the next
+// call.  Test control: HILS_Q8_UNION_UNFIT=1 takes this build for such a one.
+template <int G>
+bool fits_g()
+{
+    static std::atomic<int> known{0};
+    int regs = known.load(std::memory_order_relaxed);
+    if (regs == 0) {
+        cudaFuncAttributes a;
+        if (cudaFuncGetAttributes(&a, attend8_tc_kernel<G>) != cudaSuccess) {
+            (void)cudaGetLastError();
+            return false;
+        }
+        regs = a.numRegs;
+        known.store(regs, std::memory_order_relaxed);
+    }
+    const char *unfit = getenv("HILS_Q8_UNION_UNFIT");
+    return regs == kLaunchRegs && !(unfit && strcmp(unfit, "1") == 0);
+}
+
 template <int G>
 cudaError_t launch_g(const Dims &p, const void *Q, const uint8_t *K8, const uint8_t *V8, const float *ks, const float *vs,
                      const int32_t *sel_idx, const float *sel_score, void *O, const DeviceCtl &ctl, cudaStream_t s)
@@ -572,12 +597,7 @@ cudaError_t launch_g(const Dims &p, const void *Q, const uint8_t *K8, const uint
     const int c_max = (int)(((long long)p.q_offset + p.N - 1) / kChunk);
     const uint32_t smem = smem_bytes(p);
     auto kern = attend8_tc_kernel<G>;
-    // the warps' register shares are drawn from what the block is launched with: a build with fewer would wait forever
-    static const int regs = [] {
-        cudaFuncAttributes a;
-        return cudaFuncGetAttributes(&a, attend8_tc_kernel<G>) == cudaSuccess ? a.numRegs : -1;
-    }();
-    if (regs != kLaunchRegs) return cudaErrorInvalidConfiguration;
+    if (!fits_g<G>()) return cudaErrorInvalidConfiguration;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
     kern<<<dim3((p.N + BQ - 1) / BQ, p.Hkv, p.B), kThreads, smem, s>>>(
@@ -594,6 +614,11 @@ bool attend8_tc_supported(const Dims &p, hils_dtype in, hils_dtype out)
     if (p.G != 1 && p.G != 2 && p.G != 4 && p.G != 8 && p.G != 16) return false;
     if ((long long)p.B * p.Hkv * p.T > 0x7FFFFFFFll) return false;   // a tile's row is a 32-bit coordinate
     return smem_bytes(p) <= kSmemLimit;
+}
+
+bool attend8_tc_fits(const Dims &p)
+{
+    return p.G == 1 ? fits_g<1>() : p.G == 2 ? fits_g<2>() : p.G == 4 ? fits_g<4>() : p.G == 8 ? fits_g<8>() : fits_g<16>();
 }
 
 cudaError_t launch_attend8_tc(const Dims &p, const void *Q, const uint8_t *K8, const uint8_t *V8, const float *ks,

@@ -23,6 +23,7 @@ cudaError_t launch_landmarks8(const Cache8 &c, hils_dtype in, float scale, const
 // Chunk attention over the 8-bit cache: rows of work (every shape and type), or the union of a query block's chunks on
 // the tensor cores (bf16 in and out, d = 128, C = 64).
 bool attend8_tc_supported(const Dims &p, hils_dtype in, hils_dtype out);
+bool attend8_tc_fits(const Dims &p);   // this build's kernel has the registers that its warps share out
 cudaError_t launch_attend8_tc(const Dims &p, const void *Q, const uint8_t *K8, const uint8_t *V8, const float *ks,
                               const float *vs, const int32_t *sel_idx, const float *sel_score, void *O,
                               const DeviceCtl &ctl, cudaStream_t s);

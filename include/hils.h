@@ -360,6 +360,9 @@ HILS_API hils_status hils_landmarks_q8(const hils_problem *p, const void *K8, co
  * with d = 128 and C = 64 the union of a query block's chunks on the tensor
  * cores where that is expected to take less time.  HILS_Q8_KERNEL=rows or
  * =union forces one (the latter where it covers the shape; a test control).
+ * A build whose compiler gave the union kernel another number of registers than
+ * its warps share out takes the rows everywhere; there HILS_Q8_KERNEL=union is
+ * HILS_ERR_CUDA (HILS_Q8_UNION_UNFIT=1, a test control, behaves like one).
  */
 HILS_API hils_status hils_chunk_attend_fuse_q8_workspace_size(const hils_problem *p, size_t *bytes);
 HILS_API hils_status hils_chunk_attend_fuse_q8(const hils_problem *p, const void *Q, const void *K8, const void *V8,

@@ -100,3 +100,33 @@ def test_read_rounds_once():
         got = out[side].double().cpu().numpy()
         assert np.all(np.isnan(got[nan[side]]))
         assert np.array_equal(np.where(nan[side], 0.0, got), once[side])
+
+
+def test_a_build_without_the_union_kernel_takes_the_rows(monkeypatch):
+    """Where the union kernel's build does not have the registers its warps share out, calls that would take it run by rows;
+    only a call that asks for it by name fails, and launches nothing."""
+    p, h, dev = c8.attend_case(1, 8, 2, 512, 512, 128, 64, 4, 0, "bf16", "bf16", 650)
+    out = {}
+    for kernel in ("rows", "union", None):
+        if kernel:
+            monkeypatch.setenv("HILS_Q8_KERNEL", kernel)
+        else:
+            monkeypatch.delenv("HILS_Q8_KERNEL")
+        out[kernel] = c8.attend(p, dev)
+    c8.ok()
+    same = lambda a, b: torch.equal(a.view(torch.int16), b.view(torch.int16))   # noqa: E731
+    assert same(out[None], out["union"]) and not same(out[None], out["rows"])    # the union's, left to itself
+    monkeypatch.setenv("HILS_Q8_UNION_UNFIT", "1")
+    O = c8.attend(p, dev)
+    c8.ok()
+    assert same(O, out["rows"])
+    monkeypatch.setenv("HILS_Q8_KERNEL", "union")
+    O = torch.full_like(O, 7.0)
+    with pytest.raises(hils.HilsError) as e:
+        c8.attend(p, dev, O)
+    assert e.value.status == hils.HILS_ERR_CUDA
+    c8.ok()
+    assert torch.all(O == 7.0)
+    monkeypatch.delenv("HILS_Q8_UNION_UNFIT")
+    assert same(c8.attend(p, dev), out["union"])
+    c8.ok()
