@@ -17,10 +17,11 @@
 // used its place is filled with the pair four further on, which runs on into the warp's next chunk, so a warp has
 // 8 to 16 KB in flight or in use.
 //
-// Numbers.  A query row is scaled by a power of two to just below 2^15 and taken in f16: bf16 queries keep their 8 bits down
-// to 2^-29 of the row's largest, and below that an error of 2^-39 of it; float32 queries are two f16 pieces (22 bits).
-// P carries w_c vs_c / max_c'(w vs) and a factor 2^14 into f16 (2^-12 of the value down to 2^-28 of the row's
-// largest weight); for float32 results it is two f16 pieces.  All sums are float32; the tensor cores cut what they add to an
+// Numbers.  A query row is scaled by a power of two so that its largest element lies in [2^14, 2^15), and taken in f16, whose
+// normal numbers end at 2^-14 and whose steps at 2^-24: bf16 queries keep their 8 bits down to 2^-31 of the row's largest,
+// and below that an error of 2^-39 of it; float32 queries are two f16 pieces (2^-22 of an element, or 2^-39 of the largest).
+// P carries w_c vs_c / max_c'(w vs) and a factor 2^14 into f16 (half a step, 2^-11 of the value, down to 2^-28 of the row's
+// largest weight); for float32 results it is two f16 pieces (2^-22).  All sums are float32; the tensor cores cut what they add to an
 // accumulator off instead of rounding it, so for float32 results every product starts from zero and is added by the
 // float32 units (a chain of 264 products lost 1.6e-6 of the result, started afresh the error is 2e-7).
 //

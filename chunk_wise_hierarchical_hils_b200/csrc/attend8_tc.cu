@@ -7,14 +7,15 @@
 //
 // One CTA owns 128 rows = (128 / G) consecutive queries x the G heads of a kv-group and walks the union of their chunks,
 // two at a time.  The cache's bytes are tensor-core operands where they can be:
-//   S = Q K^T   kind::f8f6f4: key tiles as TMA brings them.  A bf16 query row is scaled by a power of two to below 2^8
-//               and is the sum of two e4m3 values (8 bits in two times 4; elements below 2^-10 of the row's largest lose
-//               up to 2^-18 of it), so two products replace a conversion of every key tile.
+//   S = Q K^T   kind::f8f6f4: key tiles as TMA brings them.  A bf16 query row is scaled by a power of two so that its
+//               largest element lies in [2^7, 2^8), and is the sum of two e4m3 values (8 bits in two times 4).  The
+//               second's step is 2^-9: elements below 2^-9 of the row's largest lose up to 2^-17 of it (2^-10 on 2^7), all
+//               others nothing.  So two products replace a conversion of every key tile.
 //   O += P V    kind::f16: the probabilities keep f16's 11 bits (three e4m3 products would be needed for
 //               that), so value tiles are widened to f16 (exact) in shared memory by four warps of their own.
 //               (By the softmax warps, between their other work, the 8K prefill took 946 us.)
-// What a row's weights w_c vs_c are divided by is the row's own largest, times 2^-14: f16 holds 2^-12 of a
-// weight down to 2^-28 of the largest, and the row is multiplied back in float32 at the end.
+// What a row's weights w_c vs_c are divided by is the row's own largest, times 2^-14: f16 rounds a weight by 2^-11 of
+// itself down to 2^-28 of the largest, and the row is multiplied back in float32 at the end.
 //
 // Roles, meeting on mbarriers (pair p = chunks 2p, 2p + 1 of the union; buffers go by p % 2):
 //   warp 0  TMA of key pairs    (K_LAND; a slot frees with the key product, QK_DONE)

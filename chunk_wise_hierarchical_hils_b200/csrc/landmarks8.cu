@@ -10,10 +10,10 @@
 // in shared memory, one in use and one being filled.  (mma.sync has an e4m3 form, but on this GPU it runs as
 // conversions and two f16 products: 1134 instructions a chunk against 735 in the f16 form.)
 //
-// Numbers.  The other operand, one row of u or p, is float32, scaled by a power of two to just below 2^15 (u by its
-// largest, p has 1): its f16 value is column 0 of the product and, for float32 results, what that leaves is column
-// 1 (22 bits together).  bf16 landmark queries are exact in column 0, and p's 2^-12 there is below the bf16 result's own
-// rounding (2^-9).  Sums are float32.
+// Numbers.  The other operand, one row of u or p, is float32, scaled by a power of two (u so that its largest lies in
+// [2^14, 2^15), p by 2^15): its f16 value is column 0 of the product and, for float32 results, what that leaves is column
+// 1 (2^-22 of the value together).  bf16 landmark queries are exact in column 0 down to 2^-31 of their largest, and p's half
+// step there, 2^-11, is below that of the bf16 result (2^-8).  Sums are float32.
 #include "cache8.h"
 #include "common.cuh"
 #include "sm100.cuh"

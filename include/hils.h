@@ -335,6 +335,8 @@ HILS_API hils_status hils_cache_read_q8(const hils_problem *p, const void *K8, c
  * float or NULL; rows of other chunks are not written, and L must not overlap
  * K8 or U.  Uses B, Hkv, T, d, C, in_dtype and scale of p.
  * A decode step that completes chunk c calls it with c, c + 1, (c + 1) * C.
+ * Precision: as hils_chunk_attend_fuse_q8 by rows, with the landmark query for a
+ * query row and the chunk's probabilities for its weights.
  */
 HILS_API hils_status hils_landmarks_q8(const hils_problem *p, const void *K8, const float *k_scale, const void *U,
                                        void *L, float *beta, int c_begin, int c_end, int t_end, void *stream);
@@ -350,12 +352,19 @@ HILS_API hils_status hils_landmarks_q8(const hils_problem *p, const void *K8, co
  * defined when the bytes the call's queries may see (t < q_offset + N, in
  * selected chunks) hold no NaN and the products stay in float range; bytes
  * behind them may be anything.
- * Precision: products accumulate in float32.  For float32 results queries and
- * probabilities enter them with 22 bits.  For bf16 results the probabilities
- * are rounded to f16 (2^-12 of a weight, down to 2^-28 of the row's largest),
- * and prefill on the tensor cores takes a bf16 query exactly but for elements
- * below 2^-10 of its largest, which lose up to 2^-18 of that.  Keys and values
- * enter exactly.
+ * Precision: float32 arithmetic throughout; keys and values enter the products
+ * exactly, queries and weights (a probability times its slot's fusion weight and
+ * value scale) rounded:
+ *   float32 results     weights within 2^-22 of themselves or 2^-39 of the row's
+ *                       largest, whichever is more
+ *   bf16 results        weights rounded to f16: 2^-11 of themselves or 2^-39 of
+ *                       the row's largest
+ *   float32 queries     elements within 2^-22 of themselves or 2^-39 of the
+ *                       row's largest
+ *   bf16 queries        exact down to 2^-31 of the row's largest element, below
+ *                       that within 2^-39 of it; in the union of chunks (below)
+ *                       exact down to 2^-9 of it, below that within 2^-17 of it
+ *                       (2^-130 for rows whose largest is below 2^-113)
  * Kernel choice: rows of queries one by one (every shape), or for bf16 prefill
  * with d = 128 and C = 64 the union of a query block's chunks on the tensor
  * cores where that is expected to take less time.  HILS_Q8_KERNEL=rows or
