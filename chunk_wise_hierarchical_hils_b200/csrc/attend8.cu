@@ -469,13 +469,21 @@ Share share_of(const Dims &p, int per_sm, int heads)
     return best;
 }
 
+// Test control: HILS_Q8_SHARE=0 .. 8 gives every row a lone warp (0) or that many blocks; -1: the rule decides.
+int forced_share()
+{
+    const char *v = getenv("HILS_Q8_SHARE");
+    return v && v[0] >= '0' && v[0] <= '0' + kMaxTeam && !v[1] ? v[0] - '0' : -1;
+}
+
 template <typename Tin, typename Tout, int D, int C>
 cudaError_t launch_t(const Dims &p, const void *Q, const uint8_t *K8, const uint8_t *V8, const float *ks, const float *vs,
                      const int32_t *sel_idx, const float *sel_score, void *O, cudaStream_t s)
 {
     constexpr int heads = heads_of(sizeof(Tin) == 4 || sizeof(Tout) == 4);
     const int hgs = (p.G + heads - 1) / heads;
-    const int cs = share_of(p, blocks_per_sm(D, C, sizeof(Tout) == 4), heads).cs;
+    const int forced = forced_share();
+    const int cs = forced >= 0 ? forced : share_of(p, blocks_per_sm(D, C, sizeof(Tout) == 4), heads).cs;
     const long long units = (long long)p.N * hgs;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(cs ? units * cs : (units + kWarps - 1) / kWarps), (unsigned)(p.B * p.Hkv));

@@ -372,6 +372,8 @@ HILS_API hils_status hils_landmarks_q8(const hils_problem *p, const void *K8, co
  * A build whose compiler gave the union kernel another number of registers than
  * its warps share out takes the rows everywhere; there HILS_Q8_KERNEL=union is
  * HILS_ERR_CUDA (HILS_Q8_UNION_UNFIT=1, a test control, behaves like one).
+ * By rows a query group's slots go to one warp or to 1 .. 8 blocks of a cluster,
+ * by expected time; HILS_Q8_SHARE=0 (one warp) .. 8 forces it (a test control).
  */
 HILS_API hils_status hils_chunk_attend_fuse_q8_workspace_size(const hils_problem *p, size_t *bytes);
 HILS_API hils_status hils_chunk_attend_fuse_q8(const hils_problem *p, const void *Q, const void *K8, const void *V8,
