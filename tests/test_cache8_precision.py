@@ -177,3 +177,81 @@ def test_queries_with_one_large_element(kernel, monkeypatch):
     err = rms_error(O, compute(p, h))
     print("root mean square of the error %.3g, allowed %.3g" % (err, WIDE_TOL[kernel]))
     assert err <= WIDE_TOL[kernel]
+
+
+# Float32 results.  Per output the roundings that are left: the query's and the weights' second pieces (2^-22 each at most),
+# an exponential (2^-22), and about 42 float32 operations of 2^-24 on the way (a logit's eight partial sums, its factors, the
+# sums over a chunk's keys and over the slots' blocks of 16 keys).  As squares: 2^-22 sqrt(3 + 42 / 16) < 2^-20.
+F32_TOL = 2.0 ** -20
+
+
+def truncated(a, b):
+    """Float32 sums cut off instead of rounded, as an accumulator that a chain of products adds to would be."""
+    s = a + b
+    f = s.astype(np.float32).astype(np.float64)
+    return np.where(np.abs(f) > np.abs(s), np.nextafter(f.astype(np.float32), np.float32(0.0)).astype(np.float64), f)
+
+
+LONG = (1, 2, 1, 2, 128 * 68, 128, 128, 64, 128 * 67 + 60, "f32", "f32", 720)     # 65 chunks of 128 keys: 516 products a chain
+
+
+def test_eleven_bits_and_truncated_chains_are_seen():
+    p, h = host_case(1, 4, 2, 12, 1200, 64, 32, 8, 900, "f32", "f32", 721)
+    want = compute(p, h)
+    two = dict(q_as=lambda q: query(q, "rows"), p_as=lambda x: pieces(x, f16, 2))
+    assert rms_error(compute(p, h, **two), want) <= F32_TOL / 2
+    assert rms_error(compute(p, h, **dict(two, q_as=lambda q: query(q, "rows", 1))), want) > 8 * F32_TOL
+    assert rms_error(compute(p, h, **dict(two, p_as=lambda x: pieces(x, f16, 1))), want) > 8 * F32_TOL
+    p, h = host_case(*LONG)
+    want = compute(p, h)
+    assert rms_error(compute(p, h, **two), want) <= F32_TOL / 2
+    assert rms_error(compute(p, h, **two, add=truncated), want) > 2 * F32_TOL
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("shape,share", [
+    ((1, 4, 2, 12, 1200, 64, 32, 8, 900), 0), ((1, 4, 2, 12, 1200, 64, 64, 8, 900), 1), ((2, 12, 2, 6, 3000, 64, 128, 9, 2500), 8),
+    ((1, 4, 2, 12, 1200, 128, 32, 8, 900), 1), ((1, 4, 2, 12, 1200, 128, 64, 8, 900), 8), ((2, 12, 2, 6, 3000, 128, 128, 9, 2500), 0),
+    (LONG[:9], 0), (LONG[:9], 8)], ids=lambda s: "x".join(map(str, s)) if isinstance(s, tuple) else str(s))
+def test_float32_results(shape, share, dtype, monkeypatch):
+    """Every (d, C), lone warps, blocks and clusters; the longest chains of products there are."""
+    monkeypatch.setenv("HILS_Q8_SHARE", str(share))
+    p, h = host_case(*shape, dtype, "f32", 722)
+    O = c8.attend(p, on_device(p, h)).double().cpu().numpy()
+    c8.ok()
+    err = rms_error(O, compute(p, h))
+    print("root mean square of the error %.3g, allowed %.3g" % (err, F32_TOL))
+    assert err <= F32_TOL
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("d,C", [(64, 32), (64, 64), (64, 128), (128, 32), (128, 64), (128, 128)])
+@pytest.mark.parametrize("umul", [1.0, 8.0])
+def test_float32_landmarks(d, C, umul):
+    """The same measure: a chunk's probabilities over its keys, whose logits have a spread of umul.  A logit's error, 2^-22 of
+    it, moves a weight by as much: umul of that."""
+    r = np.random.default_rng(730 + d + C)
+    B, Hkv, T = 2, 3, 11 * C + 7
+    data, scale = c8.make_cache(r, B, Hkv, T, d, C, T, spread=2.0)
+    nL = -(-T // C)
+    U64, U = c8.rng_rows(r, (B, Hkv, nL, d), "f32", umul)
+    # keys of 2^-2 to 2^2 times the usual: the landmark query goes with them (powers of two)
+    level = scale / np.max(scale)
+    U64, U = U64 / level[..., None], U / torch.from_numpy(level).to(c8.DEV)[..., None]
+    p = hils.problem(B, Hkv, Hkv, 1, T, d, C, 0, 0, hils.HILS_F32)
+    L, beta = torch.empty((B, Hkv, nL, d), device=c8.DEV), torch.empty((B, Hkv, nL), device=c8.DEV)
+    hils.hils_landmarks_q8(p, torch.from_numpy(data).to(c8.DEV), torch.from_numpy(scale).to(c8.DEV), U, L, beta)
+    c8.ok()
+    want, wb = np.zeros((B, Hkv, nL, d)), np.zeros((B, Hkv, nL))
+    for b in range(B):
+        for g in range(Hkv):
+            for c in range(nL):
+                k = ref.TABLE[data[b, g, c * C:min((c + 1) * C, T)]] * float(scale[b, g, c])
+                want[b, g, c], wb[b, g, c] = ref.landmarks(k, U64[b, g, c], 1.0 / math.sqrt(d))
+    got = L.double().cpu().numpy() / level[..., None]
+    err = rms_error(got, want / level[..., None])
+    eb = math.sqrt(np.mean((beta.double().cpu().numpy() - wb) ** 2))
+    print("landmarks %.3g of %.3g, entropies %.3g" % (err, F32_TOL * max(1.0, umul), eb))
+    assert err <= F32_TOL * max(1.0, umul)
+    assert eb <= F32_TOL * max(1.0, umul) * math.log(C)
