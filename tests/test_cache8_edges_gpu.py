@@ -130,3 +130,58 @@ def test_a_build_without_the_union_kernel_takes_the_rows(monkeypatch):
     monkeypatch.delenv("HILS_Q8_UNION_UNFIT")
     assert same(c8.attend(p, dev), out["union"])
     c8.ok()
+
+
+@pytest.mark.parametrize("N,q0,select", [(1, 450, None), (1, 63, None), (40, 440, None), (100, 400, "heads"), (100, 400, "queries"),
+                                         (100, 400, "simt")])
+def test_forward_with_anything_behind_the_last_token(N, q0, select, monkeypatch):
+    """A cache with room: bytes, scales and landmarks behind the last token's chunk hold anything, NaN among it, and the forward
+    gives what it gives with zeros there."""
+    if select == "simt":
+        monkeypatch.setenv("HILS_PREFILL_KERNEL", select)
+    elif select:
+        monkeypatch.setenv("HILS_SELECT_KERNEL", select)
+    r = np.random.default_rng(630 + N)
+    B, H, Hkv, T, d, C, k = 2, 8, 2, 1200, 128, 64, 3
+    p, h, dev = c8.attend_case(B, H, Hkv, N, T, d, C, k, q0, "bf16", "bf16", 640 + N)
+    nL, used = -(-T // C), (q0 + N - 1) // C + 1
+    _, L = c8.rng_rows(r, (B, Hkv, nL, d), "bf16")
+    out = []
+    for junk in (0.0, float("nan"), float("inf")):
+        L[:, :, used:] = junk
+        O = torch.full((B, H, N, d), 7.0, dtype=torch.bfloat16, device=c8.DEV)
+        ws = torch.empty(hils.hils_forward_q8_workspace_size(p), dtype=torch.uint8, device=c8.DEV)
+        hils.hils_forward_q8(p, dev["Q"], dev["K8"], dev["V8"], dev["ks"], dev["vs"], L, O, ws)
+        c8.ok()
+        out.append(O)
+    assert torch.isfinite(out[0]).all()
+    for O in out[1:]:
+        assert torch.equal(O.view(torch.int16), out[0].view(torch.int16))
+
+
+@pytest.mark.parametrize("N,kernel,dtype,out", [(1, "rows", "bf16", "bf16"), (100, "rows", "bf16", "bf16"), (100, "union", "bf16", "bf16"),
+                                                (1, "rows", "f32", "f32"), (100, "rows", "f32", "f32")])
+@pytest.mark.parametrize("v", [1e-40, 2.0 ** -126])
+def test_value_scales_below_the_normal_numbers(N, kernel, dtype, out, v, monkeypatch):
+    """Results at and below float32's smallest normal number, held to their own steps: besides the usual relative error half a
+    step of the result's subnormal numbers, and half a step of float32's for the weight of each slot, times the largest code."""
+    monkeypatch.setenv("HILS_Q8_KERNEL", kernel)
+    k = 5
+
+    def edit(h, r):
+        h["vs"] = np.where(np.isnan(h["vs"]), np.nan, np.float32(v)).astype(np.float32)
+    p, h, dev = c8.attend_case(1, 8, 2, N, 400, 128, 64, k, 250, dtype, out, 660 + N, edit=edit)
+    O = c8.attend(p, dev)
+    c8.ok()
+    o, far = O.double().cpu().numpy(), 0.0
+    step = {"bf16": 2.0 ** -134, "f32": 2.0 ** -150}[out] + (k + 1) * 448 * 2.0 ** -150
+    for g in range(2):
+        kd, vd = ref.TABLE[h["K8"][0, g]], ref.TABLE[h["V8"][0, g]]
+        for i in range(N):
+            ch, sc = np.append(h["sel"][0, g, i], (250 + i) // 64), h["score"][0, 4 * g:4 * g + 4, i].astype(np.float64)
+            want, reach, mag = ref.attend_row(h["Q"][0, 4 * g:4 * g + 4, i], kd, vd, h["ks"][0, g].astype(np.float64),
+                                              h["vs"][0, g].astype(np.float64), ch, sc, 250 + i, 64, 128 ** -0.5)
+            tol = ref.bound(reach, mag, want, out, 128, 64, np.abs(sc[np.isfinite(sc)]).max()) - 1e-37 + step
+            assert np.all(np.abs(o[0, 4 * g:4 * g + 4, i] - want) <= tol)
+            far = max(far, float(np.max(np.abs(want) / tol)))
+    assert far > 20                                         # zeros would not pass
