@@ -118,8 +118,9 @@ def _ws(ws):
 def _stream(s):
     if s is None:
         import torch
-        # the current stream's handle without building a Stream object (3 us a call)
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+        # the current stream's handle without building a Stream object (3 us a call), where torch has that
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        return raw(torch.cuda.current_device()) if raw else torch.cuda.current_stream().cuda_stream
     if isinstance(s, int):
         return s
     return s.cuda_stream
