@@ -23,7 +23,8 @@
 // P carries w_c vs_c / max_c'(w vs) and a factor 2^14 into f16 (half a step, 2^-11 of the value, down to 2^-28 of the row's
 // largest weight); for float32 results it is two f16 pieces (2^-22).  All sums are float32; the tensor cores cut what they add to an
 // accumulator off instead of rounding it, so for float32 results every product starts from zero and is added by the
-// float32 units (a chain of 264 products lost 1.6e-6 of the result, started afresh the error is 2e-7).
+// float32 units (a chain of 264 products lost 1.6e-6 of the result and one of 516 9e-6, started afresh the error is 2e-7 and
+// 4e-7, root mean square).
 //
 // A row's slots are split over the warps of one block or of a cluster of blocks, and the partial rows meet in shared
 // memory (distributed shared memory for a cluster): no workspace, no atomics, a fixed order.
@@ -447,7 +448,11 @@ __global__ void __launch_bounds__(32 * kWarps, blocks_per_sm(D, C, sizeof(Tout) 
 // often the resident warps start over.  Measured side by side: 8 rows of 65 slots, teams of eight blocks 8.5 us, six 8.8,
 // four 10.6; 128 rows of 33 slots, teams of three 17.1 us, two 17.9, four, which queue, 24; 4072 rows of 33 slots, single
 // blocks 188 us, lone warps 190, pairs 263; 65536 rows of 17 slots and 2006 rows of 5, lone warps 1.35 ms and 11 us, blocks
-// 1.65 ms and 16 us.
+// 1.65 ms and 16 us.  Those are d = 128, C = 64 but for the last.  Against every other share, forced, on 288 problems (all six
+// (d, C), bf16 and float32, four heads a group, 8 to 8192 rows of 5 to 65 slots) the rule's choice takes 1.02 times the
+// fastest's time in the median of each form, 1.03 to 1.11 on average, at most 1.5 (128 rows of 5 slots, d = 64, C = 32: 6.0 us
+// against 4.0 with one block a row; 512 rows of 17, d = 128, C = 32: 19.1 against 13.3): few or short chunks on rows that
+// just fill the card, where a start weighs more chunks than assumed and a second block more than it saves.
 struct Share {
     int cs;
     double time;
@@ -524,7 +529,8 @@ static bool use_union(const Dims &p, hils_dtype in, hils_dtype out)
     if (force && strcmp(force, "rows") == 0) return false;
     if (force && strcmp(force, "union") == 0) return true;
     if (!attend8_tc_fits(p)) return false;
-    // The union's cost is known only for selections that have nothing to do with one another, its worst case: of V
+    // The host does not know the selection: the union is priced for selections that have nothing to do with one another, its
+    // worst case (509 queries at 130K that keep the same 32 past chunks run by rows in 183 us, where the union takes 42).  Of V
     // visible chunks a block's BQ queries then want V (1 - (1 - k / V)^BQ).  A chunk of it takes 0.8 us and a
     // block's set-up 5 us (8K prefill, 62 chunks on average: 810 us against 1.32 ms by rows; 509 queries at 130K, 810 chunks
     // a block of which a query wants 33: 474 us against 184).

@@ -308,7 +308,8 @@ HILS_API hils_status hils_backward(const hils_problem *p, const void *Q, const v
  * 448 s become +-448, NaN stays NaN.  Where s is above the chunk's scale, its
  * rows before t_begin become e4m3(code * scale / s): exact, the scales being
  * powers of two, but for values that become subnormal.  So token by token and
- * all at once give the same bytes but for such values.  A chunk that the range
+ * all at once give the same bytes but for such values.  (A chunk that holds rows
+ * before t_begin has the scale that an append gave it.)  A chunk that the range
  * starts (t_begin <= c * C) takes nothing from its old bytes and scale; rows
  * behind t_end keep their bytes.  Uses B, Hkv, T, d, C and in_dtype of p;
  * 0 <= t_begin <= t_end <= T (else HILS_ERR_INVALID_ARG; an empty range
@@ -350,8 +351,10 @@ HILS_API hils_status hils_landmarks_q8(const hils_problem *p, const void *K8, co
  * what its slots count together is then unspecified.
  * The scales may be any finite floats that are not negative.  The result is
  * defined when the bytes the call's queries may see (t < q_offset + N, in
- * selected chunks) hold no NaN and the products stay in float range; bytes
- * behind them may be anything.
+ * selected chunks) hold no NaN and the products of slots with weight stay in
+ * float range (scale * d * 448 * k_scale times the row's largest |q|, and the
+ * result itself); products of slots without weight may be beyond it, and bytes
+ * behind those seen may be anything.
  * Precision: float32 arithmetic throughout; keys and values enter the products
  * exactly, queries and weights (a probability times its slot's fusion weight and
  * value scale) rounded:
