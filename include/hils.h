@@ -45,7 +45,9 @@
  * Calls are asynchronous on `stream` (a cudaStream_t; NULL = legacy default
  * stream) and validate their arguments before any launch: a status other than
  * HILS_OK from the call itself means nothing was launched.  Device-side
- * failures of bounded waits are reported by hils_sync_status().
+ * failures of bounded waits are reported by hils_sync_status().  Kernels run on
+ * the calling thread's current device: every device buffer and the stream must
+ * belong to it (pointers do not tell, so this is not checked).
  * Thread safety: calls may come from several host threads; kernels that share
  * one workspace must not overlap on the GPU.
  * Device state: the library looks up the device addresses of its own device
